@@ -591,6 +591,164 @@ OASIS_API int oasis_profile_read_n(oasis_ctx* ctx, int nkinds, double* ms_sum,
 OASIS_API int oasis_profile_read(oasis_ctx* ctx, double* ms_sum4,
                                  int64_t* count4, double* start_ms_sum4);
 
+/* ------------------------------------------------------------------------
+ * Decoding over an 8-bit cache held in HBM.  The dense anchor above reads a
+ * bf16 cache that is wholly in HBM; these calls are its quantised, paged
+ * form for whole decode steps: the drafted tokens' keys and values are
+ * rounded as they are written, the normal and draft queries attend over the
+ * pages (behind a prefix the requests may share), and the drafts are
+ * verified.  The pages describe none of them.
+ *
+ *   pages  dev [num_pages][Hkv][4128] uint8.  One unit is one KV head's block
+ *          of 16 tokens: key codes [16 tokens][128] with the two 64-byte
+ *          halves of an odd token's row exchanged (dim i of token j at byte
+ *          128 j + (i ^ 64 (j & 1))), value codes [128][16 tokens] (at 2048 +
+ *          16 i + j), 16 key exponents (at 4096 + j), 16 value exponents (at
+ *          4112 + j).  A code c is an 8-bit float e4m3 and stands, with its
+ *          token's exponent byte b, for c * 2^(b - 127).
+ *   rounding  per token and KV head, for the key and for the value: e is the
+ *          least integer with max |x| <= 448 * 2^e over the finite x, held
+ *          in [-100, 120]; b = e + 127; the code is x * 2^-e (exact)
+ *          rounded to e4m3, ties to even, so a value is off by at most 2^-4
+ *          of itself (and 2^(e - 10) near zero).  An infinity becomes the
+ *          largest code (448) of its sign, NaN stays NaN.
+ *   page_table  dev [R][max_blocks] int32: the page of each block.
+ *   seq_len     dev [R] int32: tokens in the pages, <= 16 * max_blocks; a
+ *          request with none (or fewer) is empty.  Entries of the table past
+ *          a request's blocks are not read.
+ *   slots       dev [T] int64: 16 * page + token inside the page; negative
+ *          slots are skipped.
+ * Every call is asynchronous on the caller's stream; none allocates,
+ * synchronises or leaves the current device changed, and all may be captured
+ * into graphs.  A handle's calls may run on several streams at once as long
+ * as none writes pages another one reads.  A bad page, slot or length does
+ * not fault: it raises a device error bit (BAD_BLOCK_ID for a table entry or
+ * a length, BAD_UNIT for a slot), read by oasis_q8_sync, and the block or
+ * token is left out.
+ * ------------------------------------------------------------------------ */
+#define OASIS_BF16 0
+#define OASIS_FP16 1
+#define OASIS_FP32 2
+
+typedef struct {
+  int32_t num_pages;     /* 1..2^27 */
+  int32_t max_blocks;    /* entries of a page-table row, 1..131072 */
+  int32_t num_q_heads;   /* Hq */
+  int32_t num_kv_heads;  /* Hkv; Hq % Hkv == 0 and Hq / Hkv <= 8 */
+  int32_t head_dim;      /* d; must be 128 */
+  int32_t block_size;    /* B; must be 16 */
+  float softmax_scale;   /* 0 -> 1/sqrt(d) */
+  int32_t out_fp32;      /* attention outputs in fp32 (1) or the queries' type (0) */
+  int32_t device;        /* CUDA device ordinal */
+} oasis_q8_config;
+
+typedef struct {
+  size_t pages_bytes;     /* num_pages * Hkv * 4128 */
+  size_t workspace_bytes; /* device, 256-byte aligned: the error word */
+} oasis_q8_sizes;
+
+typedef struct oasis_q8 oasis_q8;
+
+/* NULL if cfg is supported, else a static message naming the first problem.
+ * Pure host computation, like the sizes. */
+OASIS_API const char* oasis_q8_config_error(const oasis_q8_config* cfg);
+OASIS_API int oasis_q8_query_sizes(const oasis_q8_config* cfg, oasis_q8_sizes* out);
+
+/* A handle on the caller's pages (16-byte aligned, lent for its life, not
+ * initialised) and workspace; loads the kernels and clears the error word.
+ * *out is NULL on failure. */
+OASIS_API int oasis_q8_init(const oasis_q8_config* cfg, void* pages, void* workspace,
+                            oasis_q8** out);
+/* Release the handle (not the caller's buffers; work in flight is not waited
+ * for and does not need it).  NULL is accepted. */
+OASIS_API int oasis_q8_destroy(oasis_q8* q8);
+/* Message for the last failed call on the handle (never NULL). */
+OASIS_API const char* oasis_q8_last_error(const oasis_q8* q8);
+/* Wait for the device; OASIS_EDEVICE if a kernel raised an error bit since
+ * the last call (then cleared; *device_bits receives them when non-NULL). */
+OASIS_API int oasis_q8_sync(oasis_q8* q8, uint32_t* device_bits);
+
+/* Round T tokens' keys and values into the pages.  k, v: dev [T][Hkv][d] of
+ * `type` (OASIS_BF16, _FP16, _FP32), consecutive tokens k_stride / v_stride
+ * elements apart (a slice of a wider projection); 16-byte aligned, as the
+ * strides' bytes.  Slots must be distinct: of two tokens with one slot
+ * parts of both may stay.  Bytes of other slots are left as they are. */
+OASIS_API int oasis_q8_write(oasis_q8* q8, const void* k, const void* v, int type,
+                             int64_t k_stride, int64_t v_stride, const int64_t* slots,
+                             int num_tokens, void* stream);
+
+/* Read R requests' tokens back: out dev [R][Hkv][out_blocks][2][B][d] of
+ * `type`, the units of oasis_dense_attn's cache, of a host store and of
+ * oasis_prefix_attn's prefix.  Exact in bf16 and fp32 (rounded in fp16).
+ * Tokens at or past seq_len (and those of a bad page) are left as they are.
+ * out 16-byte aligned. */
+OASIS_API int oasis_q8_read(oasis_q8* q8, int num_requests, const int32_t* page_table,
+                            const int32_t* seq_len, void* out, int type, int out_blocks,
+                            void* stream);
+
+/* Attention of S = num_queries (1..4: the normal query and its drafts)
+ * queries a request over its pages.  q, out: dev [S][R][Hq][d]; q of `type`
+ * (OASIS_BF16 or _FP16).  With causal != 0 the queries are the last S tokens
+ * of the request in order: query s sees the first seq_len - (S - 1 - s)
+ * tokens; else each sees all seq_len.  A query that sees nothing gives
+ * zeros.  S * Hq / Hkv <= 32.  q and out 16-byte aligned. */
+OASIS_API int oasis_q8_attn(oasis_q8* q8, int num_requests, int num_queries, int causal,
+                            const void* q, int type, const int32_t* page_table,
+                            const int32_t* seq_len, void* out, void* stream);
+
+/* Scratch that oasis_prefix_attn wants for these sizes (device memory,
+ * 256-byte aligned; 0 is possible).  A call's scratch must not be given to
+ * another call that may run at the same time. */
+OASIS_API int oasis_prefix_workspace(const oasis_q8* q8, int num_requests, int num_queries,
+                                     int prefix_len, size_t* bytes);
+
+/* oasis_q8_attn for a batch that shares a prefix: every query sees the
+ * prefix_len tokens of prefix_kv, dev [Hkv][prefix_blocks][2][B][d] bf16
+ * (16-byte aligned; one request's units, e.g. from oasis_q8_read), then its
+ * request's pages as above (seq_len counts those alone).  The prefix is read
+ * once for the whole batch.  q must be bf16.  prefix_len <= 16 *
+ * prefix_blocks; 0 is oasis_q8_attn. */
+OASIS_API int oasis_prefix_attn(oasis_q8* q8, int num_requests, int num_queries, int causal,
+                                const void* q, int type, const void* prefix_kv,
+                                int prefix_blocks, int prefix_len, const int32_t* page_table,
+                                const int32_t* seq_len, void* out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Verification of drafted tokens, per request r with n_r = n_drafts[r] (or
+ * num_drafts) drafts x_0, x_1, ..: draft i is accepted while u_accept[r][i] *
+ * q_i(x_i) < p_i(x_i) and all before it were (64-bit products).  With k the
+ * first refused one, the next token is the least j with
+ *   w_0 + .. + w_j > u_sample[r] * (w_0 + .. + w_(V-1)),
+ * w = max(p_k - q_k, 0), or p_k where that leaves nothing, or p_(n_r) when
+ * all were accepted (k = n_r).  out_tokens[r] holds the k accepted drafts,
+ * that token, then -1; n_accept[r] = k.  Sums are held to about 48 bits.  A
+ * row without a positive entry (or with an infinite one) gives token -1; NaN
+ * counts as 0; a draft outside [0, V) gives n_accept[r] = -1 and tokens -1
+ * for its request.  Rows need not add up to one. */
+typedef struct {
+  int32_t num_requests;   /* R >= 0 */
+  int32_t num_drafts;     /* n, 0..64 */
+  int32_t vocab;          /* V, 1..2^20 */
+  int32_t type;           /* of the probabilities: OASIS_BF16, _FP16, _FP32 */
+  int32_t device;         /* CUDA device ordinal */
+  const void* target;     /* dev [R][n + 1] rows of V, target_stride elements apart */
+  const void* draft;      /* dev [R][n] rows, draft_stride apart; NULL: each draft
+                             was certain (q_i(x_i) = 1, 0 elsewhere) */
+  int64_t target_stride;  /* >= V */
+  int64_t draft_stride;
+  const int32_t* tokens;  /* dev [R][n]; may be NULL when n = 0, like u_accept */
+  const int32_t* n_drafts;  /* dev [R] (held to 0..n), or NULL: n */
+  const float* u_accept;  /* dev [R][n] in [0, 1) */
+  const float* u_sample;  /* dev [R] in [0, 1) */
+  int32_t* out_tokens;    /* dev [R][n + 1] */
+  int32_t* n_accept;      /* dev [R] */
+} oasis_verify_args;
+
+/* NULL if the call is supported, else a static message naming the first
+ * problem.  Pure host computation. */
+OASIS_API const char* oasis_verify_error(const oasis_verify_args* args);
+OASIS_API int oasis_verify_drafts(const oasis_verify_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

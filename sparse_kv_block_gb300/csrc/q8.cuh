@@ -1,0 +1,69 @@
+// q8.cuh -- the 8-bit page format shared by the quantised-cache kernels.
+//
+// A unit is one KV head's block of 16 tokens, 4128 bytes:
+//   [0, 2048)     key codes    [16 tokens][128 dims], the two 64-byte halves
+//                 of an odd token's row exchanged
+//   [2048, 4096)  value codes  [128 dims][16 tokens]
+//   [4096, 4112)  key exponents, one byte a token
+//   [4112, 4128)  value exponents
+// A code c (e4m3) with exponent byte b stands for c * 2^(b - 127).
+//
+// Why this layout.  Attention reads a unit as mma.sync m16n8k16 fragments.
+// Keys: a lane needs 16-byte pieces of a token's row, and two neighbouring
+// tokens' pieces at once; the exchange puts those in different banks.
+// Values: the contraction runs over tokens, so a lane needs consecutive
+// tokens of one dim: they are stored that way, once, when written.  A unit's
+// 4128 bytes are a multiple of 16 (one bulk copy) and 32 mod 128, so the
+// same place of four units lies in four different bank groups.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace oasis {
+
+constexpr int kQ8HalfBytes = kBlock * kHeadDim;                  // 2048
+constexpr int kQ8ExpOffset = 2 * kQ8HalfBytes;                   // 4096
+constexpr int kQ8UnitBytes = kQ8ExpOffset + 2 * kBlock;          // 4128
+constexpr int kQ8MinExp = -100, kQ8MaxExp = 120;
+
+// Byte of dim i of token j inside a unit.
+__host__ __device__ __forceinline__ int q8_key_at(int j, int i) {
+  return j * kHeadDim + (i ^ ((j & 1) << 6));
+}
+__host__ __device__ __forceinline__ int q8_value_at(int j, int i) {
+  return kQ8HalfBytes + i * kBlock + j;
+}
+
+// The least e with amax <= 448 * 2^e, held in [kQ8MinExp, kQ8MaxExp];
+// `bits` are those of amax >= 0 (fp32).  448 = 1.75 * 2^8.
+__device__ __forceinline__ int q8_exponent(uint32_t bits) {
+  const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, kQ8MinExp), kQ8MaxExp);
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2f(int e) {
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Two floats -> two e4m3 codes (lo in the low byte), to nearest even; beyond
+// 448 (an infinity) the largest code, NaN stays NaN.
+__device__ __forceinline__ uint32_t q8_pack2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d) {
+  return q8_pack2(a, b) | (q8_pack2(c, d) << 16);
+}
+
+// Two e4m3 codes -> two halves (exact).
+__device__ __forceinline__ uint32_t q8_unpack2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+
+}  // namespace oasis

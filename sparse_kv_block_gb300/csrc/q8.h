@@ -1,0 +1,76 @@
+// q8.h -- host-side launchers of the quantised-cache kernels and of the
+// draft verification.  Plain C++ structs; used by the C ABI in q8_api.cu.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace oasis {
+
+enum Q8Type { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+
+constexpr int kQ8MaxGroup = 8;     // query heads per KV head
+constexpr int kQ8MaxQueries = 4;   // queries per request
+constexpr int kVerifyMaxDrafts = 64;
+
+struct Q8WriteArgs {
+  const void* k;             // [T][Hkv][d], token stride in elements
+  const void* v;
+  int64_t k_stride, v_stride;
+  const int64_t* slots;      // [T]: page * 16 + token in the page, < 0 skips
+  uint8_t* pages;            // [num_pages][Hkv][unit]
+  uint32_t* err;
+  int64_t num_slots;         // num_pages * 16
+  int T, Hkv, type;
+};
+
+struct Q8ReadArgs {
+  const uint8_t* pages;
+  const int32_t* table;      // [R][max_blocks]
+  const int32_t* len;        // [R]
+  void* out;                 // [R][Hkv][out_blocks][2][B][d]
+  uint32_t* err;
+  int R, Hkv, num_pages, max_blocks, out_blocks, type;
+};
+
+struct Q8AttnArgs {
+  const void* q;             // [S][R][Hq][d]
+  void* out;                 // [S][R][Hq][d]
+  const uint8_t* pages;
+  const int32_t* table;      // [R][max_blocks]
+  const int32_t* len;        // [R]
+  uint32_t* err;
+  int R, S, Hq, Hkv, G, num_pages, max_blocks;
+  int causal, type, out_fp32;
+  float scale_log2;          // softmax scale * log2(e)
+  long long wait_limit;
+  // A prefix all requests share, [Hkv][prefix_blocks][2][B][d] bf16.
+  const void* prefix;
+  int prefix_blocks, prefix_len;
+};
+
+struct VerifyArgs {
+  const void* target;        // [R][n + 1] rows of V probabilities
+  const void* draft;         // [R][n] rows, or null: the drafts are certain
+  int64_t target_stride, draft_stride;  // elements between rows
+  const int32_t* tokens;     // [R][n]
+  const int32_t* n_drafts;   // [R] or null
+  const float* u_accept;     // [R][n]
+  const float* u_sample;     // [R]
+  int32_t* out_tokens;       // [R][n + 1]
+  int32_t* n_accept;         // [R]
+  int R, n, V, type;
+};
+
+cudaError_t launch_q8_write(const Q8WriteArgs& a, cudaStream_t s);
+cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
+cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
+
+// Load the kernels' code (and set their shared memory) on the current device.
+cudaError_t preload_q8_cache_kernels();
+cudaError_t preload_q8_attn_kernels();
+cudaError_t preload_verify_kernels();
+
+}  // namespace oasis

@@ -59,6 +59,28 @@ class oasis_remote_sizes(ctypes.Structure):
                 ("miss_lists_bytes", c_size_t)]
 
 
+class oasis_q8_config(ctypes.Structure):
+    _fields_ = [("num_pages", c_int32), ("max_blocks", c_int32), ("num_q_heads", c_int32),
+                ("num_kv_heads", c_int32), ("head_dim", c_int32), ("block_size", c_int32),
+                ("softmax_scale", c_float), ("out_fp32", c_int32), ("device", c_int32)]
+
+
+class oasis_q8_sizes(ctypes.Structure):
+    _fields_ = [("pages_bytes", c_size_t), ("workspace_bytes", c_size_t)]
+
+
+class oasis_verify_args(ctypes.Structure):
+    _fields_ = [("num_requests", c_int32), ("num_drafts", c_int32), ("vocab", c_int32),
+                ("type", c_int32), ("device", c_int32), ("target", c_void_p),
+                ("draft", c_void_p), ("target_stride", c_int64), ("draft_stride", c_int64),
+                ("tokens", c_void_p), ("n_drafts", c_void_p), ("u_accept", c_void_p),
+                ("u_sample", c_void_p), ("out_tokens", c_void_p), ("n_accept", c_void_p)]
+
+
+OASIS_BF16, OASIS_FP16, OASIS_FP32 = 0, 1, 2
+_TYPES = {torch.bfloat16: OASIS_BF16, torch.float16: OASIS_FP16, torch.float32: OASIS_FP32}
+Q8_UNIT_BYTES = 4128  # one KV head's block of 16 tokens in the 8-bit cache
+
 DEVERR_NOT_LOCAL = 0x8
 
 
@@ -116,6 +138,20 @@ EXPORTS = {
     "oasis_profile_read_n": (c_int, [_P, c_int, POINTER(c_double), POINTER(c_int64),
                                      POINTER(c_double)]),
     "oasis_profile_read": (c_int, [_P, POINTER(c_double), POINTER(c_int64), POINTER(c_double)]),
+    "oasis_q8_config_error": (c_char_p, [POINTER(oasis_q8_config)]),
+    "oasis_q8_query_sizes": (c_int, [POINTER(oasis_q8_config), POINTER(oasis_q8_sizes)]),
+    "oasis_q8_init": (c_int, [POINTER(oasis_q8_config), _P, _P, POINTER(c_void_p)]),
+    "oasis_q8_destroy": (c_int, [_P]),
+    "oasis_q8_last_error": (c_char_p, [_P]),
+    "oasis_q8_sync": (c_int, [_P, POINTER(c_uint32)]),
+    "oasis_q8_write": (c_int, [_P, _P, _P, c_int, c_int64, c_int64, _P, c_int, _P]),
+    "oasis_q8_read": (c_int, [_P, c_int, _P, _P, _P, c_int, c_int, _P]),
+    "oasis_q8_attn": (c_int, [_P, c_int, c_int, c_int, _P, c_int, _P, _P, _P, _P]),
+    "oasis_prefix_workspace": (c_int, [_P, c_int, c_int, c_int, POINTER(c_size_t)]),
+    "oasis_prefix_attn": (c_int, [_P, c_int, c_int, c_int, _P, c_int, _P, c_int, c_int, _P, _P,
+                                  _P, _P, c_size_t, _P]),
+    "oasis_verify_error": (c_char_p, [POINTER(oasis_verify_args)]),
+    "oasis_verify_drafts": (c_int, [POINTER(oasis_verify_args), _P]),
 }
 
 PROFILE_KINDS = ["attention", "score_topk", "admit_evict", "prefetch", "demand_score",
@@ -501,3 +537,203 @@ class Oasis:
     def set_resident(self, layer: int, res, first_step: int = 0) -> None:
         """Write the caller's resident table for `first_step` (host-to-device copy)."""
         self.res_ids[layer][first_step & 1].copy_(torch.as_tensor(res, dtype=torch.int32))
+
+
+# ------------------------------------------------- decoding over an 8-bit cache
+def _want(name: str, t: torch.Tensor, dtype, shape: tuple, device: torch.device) -> int:
+    """The address of a contiguous tensor of that type, shape and device; ValueError otherwise."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _stream_on(s, device: torch.device) -> int:
+    if s is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return s if isinstance(s, int) else s.cuda_stream
+
+
+def make_q8_config(num_pages, max_blocks, Hq, Hkv, softmax_scale=0.0, out_fp32=False, device=0,
+                   d=128, B=16) -> oasis_q8_config:
+    return oasis_q8_config(num_pages, max_blocks, Hq, Hkv, d, B, softmax_scale,
+                           1 if out_fp32 else 0, device)
+
+
+def oasis_q8_config_error(cfg: oasis_q8_config) -> Optional[str]:
+    m = lib().oasis_q8_config_error(ctypes.byref(cfg))
+    return None if m is None else m.decode()
+
+
+def oasis_q8_query_sizes(cfg: oasis_q8_config) -> oasis_q8_sizes:
+    out = oasis_q8_sizes()
+    rc = lib().oasis_q8_query_sizes(ctypes.byref(cfg), ctypes.byref(out))
+    if rc != OASIS_OK:
+        raise OasisError(rc, oasis_q8_config_error(cfg) or "q8_query_sizes failed")
+    return out
+
+
+class Q8Cache:
+    """A handle on an 8-bit paged KV cache: ``pages`` [num_pages][Hkv][4128]
+    uint8 (allocated zeroed unless passed in) and the handle's workspace.
+    Methods map one-to-one onto the C ABI calls; tensors of another type,
+    shape, device or layout than documented there are refused (ValueError).
+    """
+
+    def __init__(self, cfg: oasis_q8_config, pages: Optional[torch.Tensor] = None):
+        self.q8 = None
+        self.cfg = cfg
+        self.sizes = oasis_q8_query_sizes(cfg)
+        self.device = torch.device("cuda", cfg.device)
+        shape = (cfg.num_pages, cfg.num_kv_heads, Q8_UNIT_BYTES)
+        if pages is None:
+            pages = torch.zeros(shape, dtype=torch.uint8, device=self.device)
+        _want("pages", pages, torch.uint8, shape, self.device)
+        self.pages = pages
+        self.workspace = torch.empty(self.sizes.workspace_bytes, dtype=torch.uint8,
+                                     device=self.device)
+        handle = c_void_p()
+        rc = lib().oasis_q8_init(ctypes.byref(cfg), pages.data_ptr(), self.workspace.data_ptr(),
+                                 ctypes.byref(handle))
+        if rc != OASIS_OK:
+            raise OasisError(rc, "oasis_q8_init failed (misaligned pages, or CUDA error)")
+        self.q8 = handle.value
+
+    def _check(self, rc: int) -> None:
+        if rc != OASIS_OK:
+            raise OasisError(rc, lib().oasis_q8_last_error(self.q8).decode())
+
+    def close(self) -> None:
+        if getattr(self, "q8", None):
+            lib().oasis_q8_destroy(self.q8)
+            self.q8 = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def oasis_q8_sync(self) -> int:
+        bits = c_uint32(0)
+        rc = lib().oasis_q8_sync(self.q8, ctypes.byref(bits))
+        if rc == OASIS_EDEVICE:
+            raise OasisError(rc, f"device error bits 0x{bits.value:x}")
+        self._check(rc)
+        return bits.value
+
+    def _rows(self, name: str, x: torch.Tensor, T: int, dtype) -> int:
+        """Elements between consecutive tokens of x [T][Hkv][d], whose heads are contiguous."""
+        H, d = self.cfg.num_kv_heads, self.cfg.head_dim
+        if x.dtype != dtype or tuple(x.shape) != (T, H, d) or x.device != self.device:
+            raise ValueError(f"{name} must be {dtype} {[T, H, d]} on {self.device}, got {x.dtype} "
+                             f"{list(x.shape)} on {x.device}")
+        if T and (x.stride(2) != 1 or (H > 1 and x.stride(1) != d)):
+            raise ValueError(f"{name}: a token's heads must be contiguous")
+        return x.stride(0) if T > 1 else 0
+
+    def oasis_q8_write(self, k, v, slots, stream=None) -> None:
+        """k, v [T][Hkv][128] bf16, fp16 or fp32 (tokens may be strided), slots [T] int64."""
+        T = slots.numel()
+        if k.dtype not in _TYPES:
+            raise ValueError(f"k must be bfloat16, float16 or float32, got {k.dtype}")
+        ks, vs = self._rows("k", k, T, k.dtype), self._rows("v", v, T, k.dtype)
+        self._check(lib().oasis_q8_write(self.q8, k.data_ptr(), v.data_ptr(), _TYPES[k.dtype], ks, vs,
+                                         _want("slots", slots, torch.int64, (T,), self.device), T,
+                                         _stream_on(stream, self.device)))
+
+    def _table(self, page_table, seq_len) -> tuple:
+        R = seq_len.numel()
+        return (R, _want("page_table", page_table, torch.int32, (R, self.cfg.max_blocks), self.device),
+                _want("seq_len", seq_len, torch.int32, (R,), self.device))
+
+    def oasis_q8_read(self, page_table, seq_len, out, stream=None) -> None:
+        """out [R][Hkv][out_blocks][2][16][128] bf16, fp16 or fp32."""
+        R, table, lens = self._table(page_table, seq_len)
+        if out.dtype not in _TYPES:
+            raise ValueError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
+        blocks = int(out.shape[2]) if out.dim() == 6 else -1
+        o = _want("out", out, out.dtype, (R, self.cfg.num_kv_heads, blocks, 2, 16, 128), self.device)
+        self._check(lib().oasis_q8_read(self.q8, R, table, lens, o, _TYPES[out.dtype], blocks,
+                                        _stream_on(stream, self.device)))
+
+    def _queries(self, q, out, R: int) -> tuple:
+        if q.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
+        S = int(q.shape[0]) if q.dim() == 4 else -1
+        shape = (S, R, self.cfg.num_q_heads, self.cfg.head_dim)
+        return (S, _want("q", q, q.dtype, shape, self.device), _TYPES[q.dtype],
+                _want("out", out, torch.float32 if self.cfg.out_fp32 else q.dtype, shape, self.device))
+
+    def oasis_q8_attn(self, q, page_table, seq_len, out, causal=False, stream=None) -> None:
+        """q, out [S][R][Hq][128]."""
+        R, table, lens = self._table(page_table, seq_len)
+        S, qp, typ, o = self._queries(q, out, R)
+        self._check(lib().oasis_q8_attn(self.q8, R, S, 1 if causal else 0, qp, typ, table, lens, o,
+                                        _stream_on(stream, self.device)))
+
+    def oasis_prefix_workspace(self, R: int, S: int, prefix_len: int) -> int:
+        n = c_size_t(0)
+        rc = lib().oasis_prefix_workspace(self.q8, R, S, prefix_len, ctypes.byref(n))
+        if rc != OASIS_OK:
+            raise OasisError(rc, "prefix_workspace: bad size")
+        return n.value
+
+    def prefix_workspace(self, R: int, S: int, prefix_len: int) -> torch.Tensor:
+        """Scratch for oasis_prefix_attn calls of these sizes that follow one another."""
+        return torch.empty(self.oasis_prefix_workspace(R, S, prefix_len), dtype=torch.uint8,
+                           device=self.device)
+
+    def oasis_prefix_attn(self, q, prefix_kv, prefix_len, page_table, seq_len, out, workspace,
+                          causal=False, stream=None) -> None:
+        """q, out [S][R][Hq][128]; prefix_kv [Hkv][blocks][2][16][128] bf16; workspace from
+        prefix_workspace."""
+        R, table, lens = self._table(page_table, seq_len)
+        S, qp, typ, o = self._queries(q, out, R)
+        blocks = int(prefix_kv.shape[1]) if prefix_kv.dim() == 5 else -1
+        kv = _want("prefix_kv", prefix_kv, torch.bfloat16,
+                   (self.cfg.num_kv_heads, blocks, 2, 16, 128), self.device)
+        n = workspace.numel()
+        ws = _want("workspace", workspace, torch.uint8, (n,), self.device)
+        self._check(lib().oasis_prefix_attn(self.q8, R, S, 1 if causal else 0, qp, typ, kv, blocks,
+                                            prefix_len, table, lens, o, ws, n,
+                                            _stream_on(stream, self.device)))
+
+
+def oasis_verify_drafts(target, draft, tokens, u_accept, u_sample, out_tokens, n_accept,
+                        n_drafts=None, stream=None) -> None:
+    """target [R][n + 1][V] and draft [R][n][V] (or None: certain drafts) probabilities in bf16,
+    fp16 or fp32 (rows may be padded: a common stride between them), tokens [R][n] int32,
+    u_accept [R][n] and u_sample [R] fp32; out_tokens [R][n + 1] and n_accept [R] int32 are
+    written.  n_drafts [R] int32: drafts of each request, n where None."""
+    if target.dim() != 3 or target.dtype not in _TYPES or not target.is_cuda or target.shape[1] < 1:
+        raise ValueError("target must be a bfloat16, float16 or float32 CUDA tensor [R][n + 1][V]")
+    R, n, V = int(target.shape[0]), int(target.shape[1]) - 1, int(target.shape[2])
+    dev = target.device
+
+    def rows(name, x, m):
+        if x.dtype != target.dtype or tuple(x.shape) != (R, m, V) or x.device != dev:
+            raise ValueError(f"{name} must be {target.dtype} {[R, m, V]} on {dev}, got {x.dtype} "
+                             f"{list(x.shape)} on {x.device}")
+        stride = x.stride(1) if m > 1 else x.stride(0) if R > 1 else V
+        if V > 1 and x.numel() and x.stride(2) != 1 or (R > 1 and m > 1 and x.stride(0) != m * stride):
+            raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+        return x.data_ptr(), stride
+
+    p, ps = rows("target", target, n + 1)
+    q, qs = rows("draft", draft, n) if draft is not None and n > 0 else (None, 0)
+    a = oasis_verify_args(R, n, V, _TYPES[target.dtype], dev.index, p, q, ps, qs,
+                          _want("tokens", tokens, torch.int32, (R, n), dev),
+                          None if n_drafts is None else _want("n_drafts", n_drafts, torch.int32, (R,), dev),
+                          _want("u_accept", u_accept, torch.float32, (R, n), dev),
+                          _want("u_sample", u_sample, torch.float32, (R,), dev),
+                          _want("out_tokens", out_tokens, torch.int32, (R, n + 1), dev),
+                          _want("n_accept", n_accept, torch.int32, (R,), dev))
+    rc = lib().oasis_verify_drafts(ctypes.byref(a), _stream_on(stream, dev))
+    if rc != OASIS_OK:
+        m = lib().oasis_verify_error(ctypes.byref(a))
+        raise OasisError(rc, m.decode() if m else "oasis_verify_drafts: CUDA error")
