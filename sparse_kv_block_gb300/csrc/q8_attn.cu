@@ -1,11 +1,520 @@
-// q8_attn.cu -- attention over the 8-bit paged cache, with or without a
-// prefix that all requests share.
+// q8_attn.cu -- attention of a request's one to four queries over its 8-bit
+// pages (memory bound: 258 bytes a token and KV head, read once for all the
+// queries of that head).
+//
+// One CTA, or one cluster of CTAs where there are few (request, KV head)
+// pairs, per pair; every warp takes groups of 64 tokens (four units) through
+// a ring of its own, one bulk copy per unit.  The two products run on
+// mma.sync m16n8k16 with tokens, then dims, as M and up to 16 query columns
+// (query s, head gi: column s * G + gi) as N.  Codes become fp16 exactly;
+// which token stands for which matrix row is chosen so that a lane's 16-byte
+// loads are whole fragments and the transposed weights (movmatrix) meet the
+// value codes as they lie:
+//   S step i (0..3), row g:      token 4 i + (g & 1) of unit g / 2
+//                    row g + 8:  token 4 i + 2 + (g & 1) of unit g / 2
+//   so a lane of the transposed weights holds tokens 4 i .. 4 i + 3 of unit t,
+//   which is word i of a dim's 16 codes.
+//
+// Powers of two stay out of the roundings: a query row is scaled by its own
+// (its largest value at 2^13, so bf16 keeps all bits in fp16), a key's is
+// multiplied into the score, and a value's is added to the score's logarithm:
+// with x the score (base 2) and e the value's exponent the weight is
+//   w = 2^(x + e - M + 14),  M the running maximum of x + e,
+// the output is 2^(M - 14 - L) sum w code / sum 2^(x - L), L the running
+// maximum of x.  The largest w is 2^14: fp16 keeps all bits of weights down to
+// 2^-28 of it, and rounds those below by at most 2^-39 of it.  (One sum of
+// w 2^-e would lose tokens whose values are 2^-140 of others', rows of zeros
+// among them; the second power costs nothing here.)
 #include "q8.cuh"
 #include "q8.h"
 
 namespace oasis {
 namespace {
 
+constexpr int kGroupUnits = 4;
+constexpr int kGroupTokens = kGroupUnits * kBlock;           // 64
+constexpr int kGroupBytes = kGroupUnits * kQ8UnitBytes;      // 16512
+constexpr float kWeightLog2 = 14.f;
+
+template <int W, int kNT>
+struct Layout {
+  static constexpr int kCols = 8 * kNT;
+  static constexpr int kRing = W * kGroupBytes;              // one group a warp
+  static constexpr int kPartial = kCols * kHeadDim * 4;      // one warp's partial output
+  static_assert(W * kPartial <= kRing, "the warps' partial outputs reuse the ring");
+  static constexpr int kBars = kRing;                        // keys' and values' barrier a warp
+  static constexpr int kValid = kBars + W * 16;              // int4 for even and odd groups
+  static constexpr int kStat = kValid + W * 32;              // [W][kCols] M, L, sums
+  static constexpr int kMerged = kStat + 3 * W * kCols * 4;  // [kCols][d], then [kCols] M, L, sums
+  static constexpr int kBytes = kMerged + kPartial + 3 * kCols * 4;
+};
+
+// 16 bytes of shared memory.  (An ordinary load: the compiler may move it,
+// but not across the barrier waits, which clobber memory.)
+__device__ __forceinline__ uint4 lds128(const uint8_t* at) { return *reinterpret_cast<const uint4*>(at); }
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// 2^x, to two units in the last place (results under 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+// Four codes -> two half pairs.
+__device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 2^(m - mx); where no part has seen a score (mx = -inf) the parts are zeros,
+// or NaN, and are added as they are.
+__device__ __forceinline__ float scale_of(float m, float mx) {
+  return mx == -INFINITY ? 1.f : ex2(m - mx);
+}
+__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
+// The sums (m, l) and (m2, l2), each in units of 2^m, as one.
+__device__ __forceinline__ void join_sum(float& m, float& l, float m2, float l2) {
+  const float mx = fmaxf(m, m2);
+  l = l * scale_of(m, mx) + l2 * scale_of(m2, mx);
+  m = mx;
+}
+// What queries see nothing of is 0.
+__device__ __forceinline__ float output(float acc, float m, float sum, float msum) {
+  return sum == 0.f ? 0.f : acc / sum * ex2(m - kWeightLog2 - msum);
+}
+
+template <typename T, int W, int kNT>
+__global__ void __launch_bounds__(W * 32)
+    attn_kernel(const Q8AttnArgs a, int cluster) {
+  using Lay = Layout<W, kNT>;
+  constexpr int kCols = Lay::kCols;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int pair = blockIdx.x / cluster;
+  const int rank = static_cast<int>(cluster == 1 ? 0u : cluster_rank());
+  const int r = pair / a.Hkv, h = pair - r * a.Hkv;
+  const int col0 = blockIdx.y * kCols;                 // first column of this CTA
+  const int cols = min(a.S * a.G - col0, kCols);
+
+  uint8_t* ring = smem + warp * kGroupBytes;
+  uint64_t* key_bar = reinterpret_cast<uint64_t*>(smem + Lay::kBars) + warp * 2;
+  uint64_t* value_bar = key_bar + 1;
+  int* valid_s = reinterpret_cast<int*>(smem + Lay::kValid) + warp * 8;
+  if (lane == 0) {
+    mbar_init(key_bar, 1);
+    mbar_init(value_bar, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+
+  int len = max(a.len[r], 0);
+  if (len > a.max_blocks * kBlock) {
+    if (threadIdx.x == 0) raise_error(a.err, kErrBadBlock);
+    len = a.max_blocks * kBlock;
+  }
+  const int groups = (len + kGroupTokens - 1) / kGroupTokens;
+  const int first = rank * W + warp, step = cluster * W;
+  const int count = groups > first ? (groups - first + step - 1) / step : 0;
+
+  // Lanes 0..3 fetch a group's pages (the table's entries a turn ahead) and
+  // issue its copies: the keys as soon as the last group's have been used, so
+  // that they come in beside its second half; then the values and exponents.
+  const int32_t* row = a.table + static_cast<int64_t>(r) * a.max_blocks;
+  auto page_of = [&](int k) {
+    const int b = (first + k * step) * kGroupUnits + lane;
+    return lane < kGroupUnits && k < count && b * kBlock < len ? __ldg(row + b) : -1;
+  };
+  int page = page_of(0);
+  const uint8_t* src = nullptr;  // this lane's unit of the group issued last, if it has one
+  auto issue_keys = [&](int k) {
+    const int b = (first + k * step) * kGroupUnits + lane;
+    const bool inside = lane < kGroupUnits && b * kBlock < len;
+    const bool ok = inside && page >= 0 && page < a.num_pages;
+    if (inside && !ok) raise_error(a.err, kErrBadBlock);
+    src = ok ? a.pages + (static_cast<int64_t>(page) * a.Hkv + h) * kQ8UnitBytes : nullptr;
+    const unsigned oks = __ballot_sync(0xffffffffu, ok);
+    if (lane < kGroupUnits) valid_s[(k & 1) * 4 + lane] = ok ? min(len - b * kBlock, kBlock) : 0;
+    if (lane == 0) mbar_arrive_expect_tx(key_bar, __popc(oks) * kQ8HalfBytes);
+    __syncwarp();
+    if (ok) bulk_g2s(ring + lane * kQ8UnitBytes, src, kQ8HalfBytes, key_bar);
+    page = page_of(k + 1);
+  };
+  auto issue_values = [&]() {
+    const unsigned oks = __ballot_sync(0xffffffffu, src != nullptr);
+    constexpr int kRest = kQ8UnitBytes - kQ8HalfBytes;
+    if (lane == 0) mbar_arrive_expect_tx(value_bar, __popc(oks) * kRest);
+    __syncwarp();
+    if (src) bulk_g2s(ring + lane * kQ8UnitBytes + kQ8HalfBytes, src + kQ8HalfBytes, kRest, value_bar);
+  };
+  if (count > 0) {
+    issue_keys(0);
+    issue_values();
+  }
+
+  // Query columns as B fragments.  Step (j, w) of the contraction covers, for
+  // lane t, dims 64 j + 16 t + 4 w .. + 3.
+  uint32_t qf[kNT][8][2];
+  float f0[kNT], f1[kNT];        // score factors of columns 2 t, 2 t + 1
+  int lim0[kNT], lim1[kNT];      // tokens those columns see
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+    const int c = nt * 8 + g;
+    float x[32];
+    float amax = 0.f;
+    if (c < cols) {
+      const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const T*>(a.q) +
+          ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // dims 64 (j / 2) + 16 t + 8 (j % 2) .. + 7
+        const uint4 v = __ldg(src + (j >> 1) * 8 + t * 2 + (j & 1));
+        T e[8];
+        memcpy(e, &v, 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[j * 8 + i] = as_float(e[i]);
+          const float b = fabsf(x[j * 8 + i]);
+          if (b < INFINITY) amax = fmaxf(amax, b);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = 0.f;
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13, -100);
+    const float down = pow2f(-e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      qf[nt][i][0] = pack_f16x2(x[4 * i] * down, x[4 * i + 1] * down);
+      qf[nt][i][1] = pack_f16x2(x[4 * i + 2] * down, x[4 * i + 3] * down);
+    }
+    const float f = a.scale_log2 * pow2f(e);
+    f0[nt] = __shfl_sync(0xffffffffu, f, 8 * t);
+    f1[nt] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+    const int c0 = col0 + nt * 8 + 2 * t;
+    lim0[nt] = a.causal ? len - (a.S - 1 - c0 / a.G) : len;
+    lim1[nt] = a.causal ? len - (a.S - 1 - (c0 + 1) / a.G) : len;
+  }
+  const int all_see = a.causal ? len - (a.S - 1) : len;  // tokens every query sees
+
+  float o[kNT][8][4];
+  // Columns 2 t, 2 t + 1: M (the warp's), L and the sum (this lane's tokens).
+  float m0[kNT], m1[kNT], ml0[kNT], ml1[kNT], l0[kNT], l1[kNT];
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
+    m0[nt] = m1[nt] = ml0[nt] = ml1[nt] = -INFINITY;
+    l0[nt] = l1[nt] = 0.f;
+  }
+
+  const uint32_t key_lane = (g >> 1) * kQ8UnitBytes + (g & 1) * kHeadDim + t * 16;
+  const uint32_t value_lane = t * kQ8UnitBytes + kQ8HalfBytes + g * kBlock;
+  const int odd = (g & 1) * 8;  // shift of this lane's even / odd token in a word
+  int k = 0;
+  bool keys_late = false, values_late = false;
+  const uint8_t* sb = ring;
+  for (; k < count; ++k) {
+    if (!__all_sync(0xffffffffu, mbar_wait(key_bar, k & 1, a.wait_limit))) {
+      keys_late = true;
+      break;
+    }
+    const int base = (first + k * step) * kGroupTokens;  // position of the group's first token
+    const int4 valid = *reinterpret_cast<const int4*>(valid_s + (k & 1) * 4);
+    const bool whole = min(min(valid.x, valid.y), min(valid.z, valid.w)) == kBlock &&
+                       base + kGroupTokens <= all_see;
+
+    // Scores: S^T (64 tokens x columns), four steps of 16 tokens.
+    float s[kNT][4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) s[nt][i][0] = s[nt][i][1] = s[nt][i][2] = s[nt][i][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* at = sb + key_lane + ((j ^ (g & 1)) << 6) + i * 4 * kHeadDim;
+        const uint4 lo = lds128(at), hi = lds128(at + 2 * kHeadDim);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a0, a1, a2, a3;
+          unpack4(word(lo, w), a0, a2);
+          unpack4(word(hi, w), a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+            mma_f16_16816(s[nt][i], a0, a1, a2, a3, qf[nt][j * 4 + w][0], qf[nt][j * 4 + w][1]);
+        }
+      }
+    }
+
+    __syncwarp();
+    if (k + 1 < count) issue_keys(k + 1);
+    if (!__all_sync(0xffffffffu, mbar_wait(value_bar, k & 1, a.wait_limit))) {
+      values_late = true;
+      break;
+    }
+
+    // x, masked, and the maximum of x + e; the tokens of rows g, g + 8 of step i are bytes odd, odd
+    // + 2 of word i of unit g / 2's exponents.
+    const uint8_t* ex = sb + (g >> 1) * kQ8UnitBytes + kQ8ExpOffset;
+    const uint4 ke = lds128(ex), ve = lds128(ex + kBlock);
+    const int mine = g < 4 ? (g < 2 ? valid.x : valid.y) : (g < 6 ? valid.z : valid.w);
+    const int pos = base + (g >> 1) * kBlock + (g & 1);
+    float t0[kNT], t1[kNT], u0[kNT], u1[kNT], vl[4][2];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      t0[nt] = t1[nt] = -INFINITY;
+      u0[nt] = ml0[nt];
+      u1[nt] = ml1[nt];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int up = 0; up < 2; ++up) {  // rows g, g + 8
+        const uint32_t kb = (word(ke, i) >> (odd + 16 * up)) & 255u, vb = (word(ve, i) >> (odd + 16 * up)) & 255u;
+        const float ks = __uint_as_float(kb << 23);
+        vl[i][up] = static_cast<float>(static_cast<int>(vb) - 127);
+        const int tok = 4 * i + 2 * up;
+        const bool in = tok + (g & 1) < mine;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          float& x0 = s[nt][i][2 * up];
+          float& x1 = s[nt][i][2 * up + 1];
+          x0 *= ks * f0[nt];
+          x1 *= ks * f1[nt];
+          if (!whole) {
+            if (!in || pos + tok >= lim0[nt]) x0 = -INFINITY;
+            if (!in || pos + tok >= lim1[nt]) x1 = -INFINITY;
+          }
+          u0[nt] = fmaxf(u0[nt], x0);
+          u1[nt] = fmaxf(u1[nt], x1);
+          t0[nt] = fmaxf(t0[nt], x0 + vl[i][up]);
+          t1[nt] = fmaxf(t1[nt], x1 + vl[i][up]);
+        }
+      }
+    }
+
+    uint32_t pb[kNT][4][2];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        t0[nt] = fmaxf(t0[nt], __shfl_xor_sync(0xffffffffu, t0[nt], off));
+        t1[nt] = fmaxf(t1[nt], __shfl_xor_sync(0xffffffffu, t1[nt], off));
+      }
+      const float n0 = fmaxf(m0[nt], t0[nt]), n1 = fmaxf(m1[nt], t1[nt]);
+      // What has seen nothing keeps a maximum of -inf; its weights are 2^-inf.
+      const float b0 = finite_or_0(n0) - kWeightLog2, b1 = finite_or_0(n1) - kWeightLog2;
+      const float c0 = finite_or_0(u0[nt]), c1 = finite_or_0(u1[nt]);
+      const float al0 = ex2(m0[nt] - kWeightLog2 - b0), al1 = ex2(m1[nt] - kWeightLog2 - b1);
+      l0[nt] *= ex2(ml0[nt] - c0);
+      l1[nt] *= ex2(ml1[nt] - c1);
+      m0[nt] = n0;
+      m1[nt] = n1;
+      ml0[nt] = u0[nt];
+      ml1[nt] = u1[nt];
+      if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          o[nt][mt][0] *= al0;
+          o[nt][mt][1] *= al1;
+          o[nt][mt][2] *= al0;
+          o[nt][mt][3] *= al1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float w[4];
+#pragma unroll
+        for (int up = 0; up < 2; ++up) {
+          const float x0 = s[nt][i][2 * up], x1 = s[nt][i][2 * up + 1];
+          w[2 * up] = ex2(x0 + vl[i][up] - b0);
+          w[2 * up + 1] = ex2(x1 + vl[i][up] - b1);
+          l0[nt] += ex2(x0 - c0);
+          l1[nt] += ex2(x1 - c1);
+        }
+        pb[nt][i][0] = transposed(pack_f16x2(w[0], w[1]));
+        pb[nt][i][1] = transposed(pack_f16x2(w[2], w[3]));
+      }
+    }
+
+    // A NaN code times a zero weight is NaN.  So in a group with an end, codes
+    // past it are cleared in place, and so are NaN codes of tokens that only
+    // some queries see, whose NaN is given to the queries that see them below
+    // (bits 3 mt + token - all_see of nan_lo, nan_hi: dims 16 mt + g, + 8).
+    // Each lane treats the codes that it reads as fragments.
+    uint32_t nan_lo = 0, nan_hi = 0;
+    if (!whole) {
+      const int v = t < 2 ? (t == 0 ? valid.x : valid.y) : (t == 2 ? valid.z : valid.w);
+      const int seen = all_see - base - t * kBlock;  // of unit t, by every query
+      auto bytes = [](int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u; };
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {  // dims 16 (i / 2) + 8 (i % 2) + g
+        uint4* at = reinterpret_cast<uint4*>(ring + value_lane + i * 8 * kBlock);
+        uint4 w = *at;
+        uint32_t bad = 0;
+        auto clear = [&](uint32_t& x, int j) {  // tokens 4 j .. + 3 of unit t
+          const uint32_t keep = bytes(v - 4 * j), some = keep & ~bytes(seen - 4 * j);
+          uint32_t b = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu) & some;
+          x &= keep & ~b;
+          for (; b; b &= ~(0xffu << ((__ffs(b) - 1) & ~7)))
+            bad |= 1u << (4 * j + ((__ffs(b) - 1) >> 3) - seen);
+        };
+        clear(w.x, 0);
+        clear(w.y, 1);
+        clear(w.z, 2);
+        clear(w.w, 3);
+        *at = w;
+        if (i & 1) nan_hi |= bad << (3 * (i >> 1));
+        else nan_lo |= bad << (3 * (i >> 1));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        nan_lo |= __shfl_xor_sync(0xffffffffu, nan_lo, off);
+        nan_hi |= __shfl_xor_sync(0xffffffffu, nan_hi, off);
+      }
+    }
+
+    // Outputs: O^T (128 dims x columns) += V^T P^T.
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      const uint4 lo = lds128(sb + value_lane + mt * 16 * kBlock);
+      const uint4 hi = lds128(sb + value_lane + mt * 16 * kBlock + 8 * kBlock);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t a0, a1, a2, a3;
+        unpack4(word(lo, i), a0, a2);
+        unpack4(word(hi, i), a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+          mma_f16_16816(o[nt][mt], a0, a1, a2, a3, pb[nt][i][0], pb[nt][i][1]);
+      }
+    }
+    if (__any_sync(0xffffffffu, (nan_lo | nan_hi) != 0)) {
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        const int lo = all_see + __ffs((nan_lo >> (3 * mt)) & 7) - 1;  // first such token
+        const int hi = all_see + __ffs((nan_hi >> (3 * mt)) & 7) - 1;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          if (lo >= all_see && lo < lim0[nt]) o[nt][mt][0] = __int_as_float(0x7fffffff);
+          if (lo >= all_see && lo < lim1[nt]) o[nt][mt][1] = __int_as_float(0x7fffffff);
+          if (hi >= all_see && hi < lim0[nt]) o[nt][mt][2] = __int_as_float(0x7fffffff);
+          if (hi >= all_see && hi < lim1[nt]) o[nt][mt][3] = __int_as_float(0x7fffffff);
+        }
+      }
+    }
+    __syncwarp();
+    if (k + 1 < count) issue_values();
+  }
+  if (keys_late || values_late) {
+    if (lane == 0) raise_error(a.err, kErrTimeout);
+    // Wait for the copies still in flight before their memory is used again.
+    if (keys_late) (void)mbar_wait(key_bar, k & 1);
+    (void)mbar_wait(value_bar, k & 1);
+    if (values_late && k + 1 < count) (void)mbar_wait(key_bar, (k + 1) & 1);
+  }
+
+  // Join the warps, then the cluster's CTAs.
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      join_sum(ml0[nt], l0[nt], __shfl_xor_sync(0xffffffffu, ml0[nt], off),
+               __shfl_xor_sync(0xffffffffu, l0[nt], off));
+      join_sum(ml1[nt], l1[nt], __shfl_xor_sync(0xffffffffu, ml1[nt], off),
+               __shfl_xor_sync(0xffffffffu, l1[nt], off));
+    }
+  }
+  __syncthreads();  // every stage has been read: its memory holds partial outputs now
+  float* part = reinterpret_cast<float*>(smem);                    // [W][kCols][d]
+  float* pm = reinterpret_cast<float*>(smem + Lay::kStat);         // [W][kCols]
+  float* pml = pm + W * kCols;
+  float* pl = pml + W * kCols;
+  float* merged = reinterpret_cast<float*>(smem + Lay::kMerged);   // [kCols][d]
+  float* mm = merged + kCols * kHeadDim;                           // [kCols]
+  float* mml = mm + kCols;
+  float* ml = mml + kCols;
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+    const int c0 = nt * 8 + 2 * t;
+    float* p0 = part + (warp * kCols + c0) * kHeadDim;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      p0[mt * 16 + g] = o[nt][mt][0];
+      p0[kHeadDim + mt * 16 + g] = o[nt][mt][1];
+      p0[mt * 16 + g + 8] = o[nt][mt][2];
+      p0[kHeadDim + mt * 16 + g + 8] = o[nt][mt][3];
+    }
+    if (g == 0) {
+      pm[warp * kCols + c0] = m0[nt];
+      pm[warp * kCols + c0 + 1] = m1[nt];
+      pml[warp * kCols + c0] = ml0[nt];
+      pml[warp * kCols + c0 + 1] = ml1[nt];
+      pl[warp * kCols + c0] = l0[nt];
+      pl[warp * kCols + c0 + 1] = l1[nt];
+    }
+  }
+  __syncthreads();
+  auto put = [&](int c, int d, float v) {
+    const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
+    const int64_t at = ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim + d;
+    if (a.out_fp32) static_cast<float*>(a.out)[at] = v;
+    else static_cast<T*>(a.out)[at] = static_cast<T>(v);
+  };
+  for (int e = threadIdx.x; e < cols * kHeadDim; e += W * 32) {
+    const int c = e / kHeadDim, d = e % kHeadDim;
+    float mx = -INFINITY, msum = -INFINITY, acc = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) mx = fmaxf(mx, pm[w * kCols + c]);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      acc = fmaf(scale_of(pm[w * kCols + c], mx), part[(w * kCols + c) * kHeadDim + d], acc);
+      join_sum(msum, sum, pml[w * kCols + c], pl[w * kCols + c]);
+    }
+    if (cluster == 1) {
+      put(c, d, output(acc, mx, sum, msum));
+    } else {
+      merged[e] = acc;
+      if (d == 0) {
+        mm[c] = mx;
+        mml[c] = msum;
+        ml[c] = sum;
+      }
+    }
+  }
+  if (cluster == 1) return;
+  cluster_sync();
+  for (int e = rank * W * 32 + threadIdx.x; e < cols * kHeadDim; e += cluster * W * 32) {
+    const int c = e / kHeadDim;
+    float mx = -INFINITY, msum = -INFINITY, acc = 0.f, sum = 0.f;
+    for (int i = 0; i < cluster; ++i) mx = fmaxf(mx, load_remote(mm + c, i));
+    for (int i = 0; i < cluster; ++i) {
+      acc = fmaf(scale_of(load_remote(mm + c, i), mx), load_remote(merged + e, i), acc);
+      join_sum(msum, sum, load_remote(mml + c, i), load_remote(ml + c, i));
+    }
+    put(c, e % kHeadDim, output(acc, mx, sum, msum));
+  }
+  cluster_sync();  // no CTA leaves while another still reads its shared memory
+}
 constexpr int kWarps = 4;
 
 // One CTA per query vector (query s of request r, head hq): each warp takes
@@ -26,7 +535,7 @@ __global__ void simple_kernel(const Q8AttnArgs a) {
   float q[4];
   const T* qp = static_cast<const T*>(a.q) + static_cast<int64_t>(vec) * kHeadDim + lane * 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = static_cast<float>(qp[i]) * a.scale_log2;
+  for (int i = 0; i < 4; ++i) q[i] = as_float(qp[i]) * a.scale_log2;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   auto token = [&](const float* k, const float* v) {
     float x = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
@@ -84,25 +593,75 @@ __global__ void simple_kernel(const Q8AttnArgs a) {
   else static_cast<T*>(a.out)[at] = static_cast<T>(v);
 }
 
+
+#ifndef Q8_W
+#define Q8_W 4
+#endif
+constexpr int kAttnWarps = Q8_W;
+
+template <typename T, int kNT>
+cudaError_t configure() {
+  return cudaFuncSetAttribute(attn_kernel<T, kAttnWarps, kNT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Layout<kAttnWarps, kNT>::kBytes);
+}
+
+template <typename T, int kNT>
+cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
+  const int64_t ctas = static_cast<int64_t>(a.R) * a.Hkv * col_groups;
+  const int groups = (a.max_blocks + kGroupUnits - 1) / kGroupUnits;
+  // CTAs of a pair: while the card is not full, as many as have a group for
+  // every warp; beyond that up to about three rounds of CTAs (the last round's
+  // idle SMs), each warp keeping eight groups or more to spread its start and
+  // join over.  GB300, 64 requests x 8 heads x 16384 tokens, two queries: 350
+  // us at two, 325 at four, 350 at eight; 32 x 8 x 8192: 123, 108, 115; one
+  // request of 4096 (the host's issue included): 20, 14, 11.
+  const int64_t slots = 152 * (kNT == 1 ? 3 : 2);
+  int cluster = 1;
+  while (cluster < 8 && 2 * cluster * kAttnWarps * (ctas * cluster < slots / 2 ? 1 : 8) <= groups &&
+         ctas * cluster < 3 * slots)
+    cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.R) * a.Hkv * cluster, col_groups);
+  cfg.blockDim = dim3(kAttnWarps * 32);
+  cfg.dynamicSmemBytes = Layout<kAttnWarps, kNT>::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_kernel<T, kAttnWarps, kNT>, a, cluster);
+}
+
+template <typename T>
+cudaError_t launch_n(const Q8AttnArgs& a, cudaStream_t s) {
+  const int cols = a.S * a.G;
+  if (cols <= 8) return launch_t<T, 1>(a, 1, s);
+  return launch_t<T, 2>(a, (cols + 15) / 16, s);
+}
+
 }  // namespace
 
 cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.S) * a.R * a.Hq;
-  if (grid == 0) return cudaSuccess;
-  if (a.type == kBf16) simple_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, s>>>(a);
-  else simple_kernel<__half><<<grid, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.R == 0) return cudaSuccess;
+  if (a.prefix_len > 0) {
+    simple_kernel<__nv_bfloat16><<<static_cast<unsigned>(a.S) * a.R * a.Hq, kWarps * 32, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  return a.type == kBf16 ? launch_n<__nv_bfloat16>(a, s) : launch_n<__half>(a, s);
 }
 
+// Their code and shared memory on the current device.
 cudaError_t preload_q8_attn_kernels() {
   cudaFuncAttributes at;
-  const void* fns[] = {reinterpret_cast<const void*>(simple_kernel<__nv_bfloat16>),
-                       reinterpret_cast<const void*>(simple_kernel<__half>)};
-  for (const void* f : fns) {
-    const cudaError_t e = cudaFuncGetAttributes(&at, f);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  cudaError_t e = configure<__nv_bfloat16, 1>();
+  if (e == cudaSuccess) e = configure<__nv_bfloat16, 2>();
+  if (e == cudaSuccess) e = configure<__half, 1>();
+  if (e == cudaSuccess) e = configure<__half, 2>();
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, simple_kernel<__nv_bfloat16>);
+  return e;
 }
 
 }  // namespace oasis

@@ -9,9 +9,14 @@ torch.finfo(t).eps / 2 of the value.  The attention kernels
   <= 2^-23 A),
 * round the weights to fp16 (8-bit pages) or bf16 (prefix) before the second
   product, and sum at most N terms in fp32.
+* round weights under 2^-28 of the largest weighted one by at most 2^-39 of it
+  (fp16's least step is 2^-24, the largest weight 2^14): with E the value scale
+  448 * 2^e of the token whose p * 2^e is largest, a token adds at most
+  2^-39 * 448 * 2^e * p_there <= 2^-39 E to the numerator's sum p v, which is
+  divided by l >= p_there; N tokens add at most 2^-39 N E to the output.
 The weights' common relative error e = 2^-11 (2^-8) + ln 2 * 270 * 2^-23 * A +
 2^-20 enters numerator and denominator: |o - o'| <= 2 e * sum p |v| / l, plus
-the output's own rounding.
+2^-39 N E and the output's own rounding.
 """
 import math
 
@@ -88,8 +93,13 @@ def write(pages, k, v, slots):
 def tokens(pages, row, n):
     """(keys, values) [H][n][128] fp64 of one request's first n tokens; tokens of bad pages are
     left out (a third result names the tokens that are there)."""
+    return tokens_and_scales(pages, row, n)[:3]
+
+
+def tokens_and_scales(pages, row, n):
+    """`tokens` and the values' scales 2^e [H][n]."""
     P, H = pages.shape[:2]
-    K, V, at = [], [], []
+    K, V, at, E = [], [], [], []
     i = np.arange(D)
     for t in range(n):
         p, j = int(row[t // B]), t % B
@@ -98,11 +108,12 @@ def tokens(pages, row, n):
         u = pages[p]
         K.append(TABLE[u[:, key_at(j, i)]] * 2.0 ** (u[:, 4096 + j].astype(np.float64) - 127)[:, None])
         V.append(TABLE[u[:, value_at(j, i)]] * 2.0 ** (u[:, 4112 + j].astype(np.float64) - 127)[:, None])
+        E.append(2.0 ** (u[:, 4112 + j].astype(np.float64) - 127))
         at.append(t)
     if not K:
         z = np.zeros((H, 0, D))
-        return z, z, np.zeros(0, dtype=np.int64)
-    return np.stack(K, 1), np.stack(V, 1), np.asarray(at)
+        return z, z, np.zeros(0, dtype=np.int64), np.zeros((H, 0))
+    return np.stack(K, 1), np.stack(V, 1), np.asarray(at), np.stack(E, 1)
 
 
 def attention(q, pages, table, lens, causal, scale=None, prefix=None, p_half=2.0 ** -11, out=None):
@@ -117,7 +128,7 @@ def attention(q, pages, table, lens, causal, scale=None, prefix=None, p_half=2.0
     bound = np.zeros_like(o)
     for r in range(R):
         n = max(0, int(lens[r]))
-        k, v, at = tokens(pages, table[r], n)
+        k, v, at, E = tokens_and_scales(pages, table[r], n)
         for s in range(S):
             see = at < (n - (S - 1 - s) if causal else n)
             kk, vv = k[:, see], v[:, see]
@@ -134,6 +145,9 @@ def attention(q, pages, table, lens, causal, scale=None, prefix=None, p_half=2.0
                 o[s, r, hq] = p @ vv[h] / l
                 e = p_half + math.log(2) * 270 * 2.0 ** -23 * A + 2.0 ** -20
                 bound[s, r, hq] = 2 * e * (p @ np.abs(vv[h])) / l
+                if see.any():
+                    w = p[-int(see.sum()):] * E[h, see]
+                    bound[s, r, hq] += 2.0 ** -39 * see.sum() * 448 * E[h, see][w.argmax()]
     bound += HALF[out] * np.abs(o) * 1.01 + 1e-30 if out is not None else 0.0
     return o, bound
 

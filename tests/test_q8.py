@@ -286,6 +286,46 @@ def test_attention_nan_reaches_only_its_head(dev):
     assert bad[:, 9].all() and bad.sum() == 2
 
 
+@pytest.mark.parametrize("n", [7, 64, 67, 130])
+def test_attention_nan_in_a_drafted_token_stays_with_its_readers(dev, n):
+    """A NaN value of the last token is seen by the last query alone, one of the token before by
+    two; NaN keys likewise."""
+    g = gen(17 + n)
+    c = cache_of(12, 10, 5, 1, out_fp32=True)
+    pages = fill(c, g).copy()
+    table = Q.table_of([n], 12, 10, g)
+    clean = pages.copy()
+    at = lambda t: (int(table[0, t // 16]), 0)  # noqa: E731
+    pages[at(n - 1)][Q.value_at((n - 1) % 16, 100)] = 0xFF
+    pages[at(n - 2)][Q.value_at((n - 2) % 16, 9)] = 0x7F
+    c.pages.copy_(torch.from_numpy(pages))
+    q = torch.randn(4, 1, 5, 128, generator=g).to(BF)
+    out = attend(c, q.cuda(), table, [n], True).cpu()
+    bad = torch.isnan(out[:, 0])
+    want = torch.zeros_like(bad)
+    want[3, :, 100] = True
+    want[2:, :, 9] = True
+    assert torch.equal(bad, want)
+    o, b = Q.attention(q, clean, table.numpy(), [n], True, out=FP)
+    close(torch.where(torch.isnan(out), torch.from_numpy(o).float(), out), o, b)
+    pages = clean.copy()
+    pages[at(n - 1)][Q.key_at((n - 1) % 16, 5)] = 0x7F
+    c.pages.copy_(torch.from_numpy(pages))
+    out = attend(c, q.cuda(), table, [n], True).cpu()
+    assert torch.isnan(out[3]).all() and torch.isfinite(out[:3]).all()
+
+
+def test_attention_nan_query_gives_nan(dev):
+    g = gen(18)
+    c = cache_of(12, 10, 4, 1, out_fp32=True)
+    fill(c, g)
+    table = Q.table_of([70], 12, 10, g)
+    q = torch.randn(2, 1, 4, 128, generator=g).to(BF)
+    q[1, 0, 2, 77] = float("nan")
+    out = attend(c, q.cuda(), table, [70], False).cpu()
+    assert torch.isnan(out[1, 0, 2]).all() and int(torch.isnan(out).sum()) == 128
+
+
 def test_attention_bad_pages_are_left_out(dev):
     g = gen(14)
     c = cache_of(20, 8, 4, 2, out_fp32=True)
