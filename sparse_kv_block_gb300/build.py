@@ -20,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liboasis.so")
 SOURCES = ["api.cu", "attn.cu", "score_topk.cu", "admit_gather.cu", "noalloc.cu",
-           "q8.cu", "q8_attn.cu", "verify.cu", "q8_api.cu"]
+           "q8.cu", "q8_attn.cu", "prefix.cu", "verify.cu", "q8_api.cu"]
 INCLUDE_DIRS = [CSRC, os.path.join(ROOT, "include")]
 _INCLUDE_RE = re.compile(r'^\s*#\s*include\s*"([^"]+)"', re.M)
 

@@ -1,0 +1,398 @@
+// prefix.cu -- attention of a whole batch over the prefix it shares.
+//
+// The queries of all requests that read one KV head are the rows of one
+// matrix (row (r * S + s) * G + gi), so the prefix is read once, and with
+// many requests the work is two matrix products: 4 * 128 operations a row and
+// token against 512 bytes a token, bound by the tensor cores from about 300
+// rows on (below, by HBM).
+//
+// One CTA per 128 or 256 rows, KV head and share of the prefix: warps 0..7
+// are the softmax of two tiles of 128 rows, one thread a row; warp 8 brings
+// tiles of 128 tokens (TMA, 128-byte swizzle, a ring of four 32 KiB stages
+// that holds keys and values in turn); one thread of warp 9 issues the
+// products (tcgen05, M = N = 128).  Scores and outputs stay in tensor memory
+// (512 columns: two tiles of 128 + 128); the weights go back there as bf16
+// over the scores they came from and are the second product's A operand.
+// While one tile's weights are formed the other's products run.  The running
+// maximum is only moved when a row's grows by more than 2^8, so the outputs
+// are seldom rescaled.
+//
+// Each share writes its rows' unnormalised outputs, maxima and sums; the
+// attention over the requests' own pages joins them in its last step.
+#include "common.cuh"
+#include "q8.h"
+
+namespace oasis {
+namespace {
+
+constexpr int kTile = 128;                                 // rows, tokens
+constexpr int kHalfTile = kTile * 128;                     // 64 dims of a tile: 16 KiB
+constexpr int kStageBytes = 2 * kHalfTile;                 // 32 KiB
+constexpr int kRingStages = 4;
+constexpr float kLazy = 8.f;                               // growth of a maximum let pass (log2)
+
+template <int kTiles>
+struct PrefixLayout {
+  static constexpr int kThreads = kTiles * 128 + 64;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kTiles * kStageBytes;
+  static constexpr int kBars = kRing + kRingStages * kStageBytes;
+  static constexpr int kBytes = kBars + 256 + 1024;        // + alignment
+  static constexpr int kColumns = kTiles * 256;            // tensor memory
+};
+
+// ------------------------------------------------------------ tcgen05
+__device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+// A descriptor of a tile in shared memory, 128-byte swizzle: 8 rows of 128
+// bytes 1024 apart; `leading` bytes between 64-column pieces (only for an
+// operand whose columns are the outer index).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t at, uint32_t leading) {
+  return static_cast<uint64_t>((at & 0x3ffffu) >> 4) | static_cast<uint64_t>(leading >> 4) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// bf16 x bf16 -> fp32, M = N = 128; bit 16: B's columns are contiguous.
+constexpr uint32_t kInstr = 1u << 4 | 1u << 7 | 1u << 10 | (128u >> 3) << 17 | (128u >> 4) << 24;
+constexpr uint32_t kInstrBt = kInstr | 1u << 16;
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kInstr), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(kInstrBt), "r"(add)
+      : "memory");
+}
+// Arrive on `bar` when this thread's products so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// 32 columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 64 dims of 8 blocks' keys (z = 0) or values (z = 1).
+__device__ __forceinline__ void load_blocks(void* dst, const CUtensorMap* map, int x, int z, int block,
+                                            int head, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(z), "r"(block), "r"(head),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int kTiles>
+__global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
+    prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map) {
+  using Lay = PrefixLayout<kTiles>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::kBars);
+  uint64_t* full = bars;                       // [4] a stage has landed
+  uint64_t* empty = bars + kRingStages;        // [4] its products are done
+  uint64_t* s_full = bars + 2 * kRingStages;   // [2] scores of a tile
+  uint64_t* p_full = s_full + 2;               // [2] its weights (128 threads)
+  uint64_t* o_done = p_full + 2;               // [2] its outputs
+  uint64_t* drain = o_done + 2;
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row_tile = blockIdx.x % a.row_tiles;
+  const int h = (blockIdx.x / a.row_tiles) % a.Hkv;
+  const int split = blockIdx.x / a.row_tiles / a.Hkv;
+  const int per_request = a.S * a.G;
+  const int rows = a.R * per_request;
+  const int row0 = row_tile * kTiles * kTile;
+  const int all_tiles = (a.prefix_len + kTile - 1) / kTile;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * split / a.splits);
+  const int n = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / a.splits) - tile0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * kRingStages + 2; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&p_full[i], 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&o_done[i], 1);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+    prefetch_tensormap(&map);
+  }
+  if (warp == kTiles * 4 + 1) tmem_alloc(tmem_s, Lay::kColumns);
+  // The query rows, 16 bytes a step, as the swizzle places them.
+  for (int e = threadIdx.x; e < kTiles * kTile * 16; e += Lay::kThreads) {
+    const int rr = e >> 4, ch = e & 15, row = row0 + rr;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (row < rows) {
+      const int r = row / per_request, c = row % per_request;
+      v = __ldg(reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(a.q) +
+          ((static_cast<int64_t>(c / a.G) * a.R + r) * a.Hq + h * a.G + c % a.G) * kHeadDim + ch * 8));
+    }
+    uint8_t* tile = smem + Lay::kQ + (rr / kTile) * kStageBytes + (ch >> 3) * kHalfTile;
+    *reinterpret_cast<uint4*>(tile + (rr % kTile) * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_s;
+
+  bool ok = true;
+  if (warp == kTiles * 4) {
+    // ---- loads: stage 2 i is tile i's keys, 2 i + 1 its values
+    if (lane == 0) {
+      int loaded = 0;
+      for (int j = 0; j < 2 * n && ok; ++j) {
+        const int st = j % kRingStages;
+        if (j >= kRingStages) ok = mbar_wait(&empty[st], (j / kRingStages - 1) & 1, a.wait_limit);
+        if (!ok) break;
+        uint8_t* dst = smem + Lay::kRing + st * kStageBytes;
+        const int block = (tile0 + (j >> 1)) * (kTile / kBlock);
+        mbar_arrive_expect_tx(&full[st], kStageBytes);
+        load_blocks(dst, &map, 0, j & 1, block, h, &full[st]);
+        load_blocks(dst + kHalfTile, &map, 64, j & 1, block, h, &full[st]);
+        loaded = j + 1;
+      }
+      // No copy may outlive the CTA, whatever the other warps met.
+      for (int j = max(loaded - kRingStages, 0); j < loaded; ++j)
+        (void)mbar_wait(&full[j % kRingStages], (j / kRingStages) & 1);
+    }
+  } else if (warp == kTiles * 4 + 1) {
+    // ---- products
+    if (lane == 0) {
+      auto stage = [&](int j) { return smem_u32(smem + Lay::kRing + (j % kRingStages) * kStageBytes); };
+      auto landed = [&](int j) { return mbar_wait(&full[j % kRingStages], (j / kRingStages) & 1, a.wait_limit); };
+      auto scores = [&](int t, int i) {
+        const uint32_t q = smem_u32(smem + Lay::kQ + t * kStageBytes), k = stage(2 * i);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {  // 16 dims a step
+          const uint32_t off = (s >> 2) * kHalfTile + (s & 3) * 32;
+          mma_ss(tmem + t * 128, smem_desc(q + off, 16), smem_desc(k + off, 16), s > 0);
+        }
+        mma_commit(&s_full[t]);
+        if (t == kTiles - 1) mma_commit(&empty[(2 * i) % kRingStages]);
+      };
+      ok = landed(0);
+      if (ok) {
+        fence_after();
+        for (int t = 0; t < kTiles; ++t) scores(t, 0);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        ok = landed(2 * i + 1);
+        const uint32_t v = stage(2 * i + 1);
+        for (int t = 0; t < kTiles && ok; ++t) {
+          ok = mbar_wait(&p_full[t], i & 1, a.wait_limit);
+          if (!ok) break;
+          fence_after();
+#pragma unroll
+          for (int s = 0; s < 8; ++s)  // 16 tokens a step
+            mma_ts(tmem + kTiles * 128 + t * 128, tmem + t * 128 + s * 8, smem_desc(v + s * 16 * 128, kHalfTile),
+                   i > 0 || s > 0);
+          mma_commit(&o_done[t]);
+          if (t == kTiles - 1) mma_commit(&empty[(2 * i + 1) % kRingStages]);
+          if (i + 1 < n) {
+            if (t == 0) ok = landed(2 * i + 2);
+            if (!ok) break;
+            scores(t, i + 1);
+          }
+        }
+      }
+      mma_commit(drain);
+      (void)mbar_wait(drain, 0);
+    }
+  } else {
+    // ---- softmax of row `lane` of this warp's quarter of tile t
+    const int t = warp >> 2;
+    const int rr = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + kTiles * 128 + t * 128;
+    const float sc = a.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < n; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], i & 1, a.wait_limit));
+      if (!ok) break;
+      fence_after();
+      float s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
+      tmem_wait_ld();
+      const int valid = a.prefix_len - (tile0 + i) * kTile;
+      if (valid < kTile) {
+#pragma unroll
+        for (int c = 0; c < kTile; ++c)
+          if (c >= valid) s[c] = -INFINITY;
+        if (t == 0) {
+          // Values past the end may be anything, and 0 * NaN is NaN: clear them.
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[(2 * i + 1) % kRingStages],
+                                                 ((2 * i + 1) / kRingStages) & 1, a.wait_limit));
+          if (!ok) break;
+          if (rr >= valid) {
+            uint8_t* at = smem + Lay::kRing + ((2 * i + 1) % kRingStages) * kStageBytes + rr * 128;
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              *reinterpret_cast<uint4*>(at + (c >> 3) * kHalfTile + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      float alpha = 1.f;
+      if (top > m + kLazy || m == -INFINITY) {
+        const float to = fmaxf(top, m);
+        alpha = m == -INFINITY ? 0.f : ex2(m - to);
+        m = to;
+      }
+      if (__any_sync(0xffffffffu, alpha != 1.f) && i > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (i - 1) & 1, a.wait_limit));
+        if (!ok) break;
+        fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld32(o_at + c * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] *= alpha;
+          tmem_st32(o_at + c * 32, reinterpret_cast<const uint32_t*>(o));
+        }
+      }
+      l *= alpha;
+      const float off = m == -INFINITY ? 0.f : -m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float p0 = ex2(fmaf(s[c * 64 + 2 * j], sc, off)), p1 = ex2(fmaf(s[c * 64 + 2 * j + 1], sc, off));
+          sum[(2 * j) & 3] += p0;
+          sum[(2 * j + 1) & 3] += p1;
+          w[j] = pack_bf16x2(p0, p1);
+        }
+        tmem_st32(s_at + c * 32, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      fence_before();
+      mbar_arrive(&p_full[t]);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (n - 1) & 1, a.wait_limit));
+    if (ok) {
+      fence_after();
+      const int row = row0 + t * kTile + rr;
+      const int64_t at = (static_cast<int64_t>(split) * a.Hkv + h) * rows + row;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld32(o_at + c * 32, o);
+        tmem_wait_ld();
+        if (row < rows) {
+          float4* dst = reinterpret_cast<float4*>(a.part + at * kHeadDim + c * 32);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+      if (row < rows) a.stat[at] = make_float2(m, l);
+    }
+  }
+  if (!ok && lane == 0) raise_error(a.err, kErrTimeout);
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == kTiles * 4 + 1) tmem_free(tmem, Lay::kColumns);
+}
+
+}  // namespace
+
+PrefixShape prefix_shape(int R, int S, int G, int Hkv, int prefix_len) {
+  PrefixShape p{};
+  const int64_t rows = static_cast<int64_t>(R) * S * G;
+  p.rows = rows;
+  p.tiles = rows > kTile ? 2 : 1;
+  p.row_tiles = static_cast<int>((rows + p.tiles * kTile - 1) / (p.tiles * kTile));
+  const int64_t units = static_cast<int64_t>(p.row_tiles) * Hkv;
+  const int all = (prefix_len + kTile - 1) / kTile;
+  int64_t splits = units > 0 ? 152 / units : 1;
+  if (splits > all) splits = all;
+  p.splits = splits < 1 ? 1 : static_cast<int>(splits);
+  const int64_t vectors = p.splits * static_cast<int64_t>(Hkv) * rows;
+  p.part_bytes = static_cast<size_t>(vectors) * kHeadDim * 4;
+  p.bytes = p.part_bytes + static_cast<size_t>(vectors) * 8;
+  return p;
+}
+
+namespace {
+template <int kTiles>
+cudaError_t launch_tiles(const PrefixArgs& a, const CUtensorMap& map, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(a.row_tiles) * a.Hkv * a.splits;
+  prefix_kernel<kTiles><<<grid, PrefixLayout<kTiles>::kThreads, PrefixLayout<kTiles>::kBytes, s>>>(a, map);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_prefix(const PrefixArgs& a, int tiles, const CUtensorMap& map, cudaStream_t s) {
+  return tiles == 2 ? launch_tiles<2>(a, map, s) : launch_tiles<1>(a, map, s);
+}
+
+cudaError_t preload_prefix_kernels() {
+  cudaError_t e = cudaFuncSetAttribute(prefix_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       PrefixLayout<1>::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prefix_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PrefixLayout<2>::kBytes);
+  return e;
+}
+
+}  // namespace oasis

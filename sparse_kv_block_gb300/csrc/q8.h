@@ -45,9 +45,31 @@ struct Q8AttnArgs {
   int causal, type, out_fp32;
   float scale_log2;          // softmax scale * log2(e)
   long long wait_limit;
-  // A prefix all requests share, [Hkv][prefix_blocks][2][B][d] bf16.
-  const void* prefix;
-  int prefix_blocks, prefix_len;
+  // What the launch before this one found for a prefix that all requests
+  // share (splits > 0), of row r * S * G + s * G + gi: outputs [splits][Hkv]
+  // [R * S * G][d] in units of 2^m over their sums, and (m, sum).
+  const float* part;
+  const float2* stat;
+  int splits;
+};
+
+// Shares and row tiles of the prefix attention, and its scratch.
+struct PrefixShape {
+  int64_t rows;      // R * S * G
+  int tiles;         // 128-row tiles a CTA, 1 or 2
+  int row_tiles;     // CTAs over the rows
+  int splits;        // shares of the prefix
+  size_t part_bytes, bytes;
+};
+
+struct PrefixArgs {
+  const void* q;             // [S][R][Hq][d] bf16
+  float* part;               // [splits][Hkv][rows][d]
+  float2* stat;              // [splits][Hkv][rows]
+  uint32_t* err;
+  int R, S, Hq, Hkv, G, prefix_len, row_tiles, splits;
+  float scale_log2;
+  long long wait_limit;
 };
 
 struct VerifyArgs {
@@ -66,11 +88,16 @@ struct VerifyArgs {
 cudaError_t launch_q8_write(const Q8WriteArgs& a, cudaStream_t s);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
 cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s);
+PrefixShape prefix_shape(int R, int S, int G, int Hkv, int prefix_len);
+// The map covers the prefix [Hkv][blocks][2][B][d] with boxes of 8 blocks'
+// keys or values, 64 dims.
+cudaError_t launch_prefix(const PrefixArgs& a, int tiles, const CUtensorMap& map, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 
 // Load the kernels' code (and set their shared memory) on the current device.
 cudaError_t preload_q8_cache_kernels();
 cudaError_t preload_q8_attn_kernels();
+cudaError_t preload_prefix_kernels();
 cudaError_t preload_verify_kernels();
 
 }  // namespace oasis

@@ -1,5 +1,7 @@
 // q8_api.cu -- the C ABI of decoding over the 8-bit cache (include/oasis.h):
 // argument checks, the handle and the launches.
+#include <cudaTypedefs.h>
+
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -95,7 +97,8 @@ OASIS_API int oasis_q8_init(const oasis_q8_config* cfg, void* pages, void* works
   if (!aligned(pages, 16) || !aligned(workspace, 256)) return OASIS_EINVAL;
   OnDevice dev(cfg->device);
   if (dev.error() != cudaSuccess) return OASIS_ECUDA;
-  if (preload_q8_cache_kernels() != cudaSuccess || preload_q8_attn_kernels() != cudaSuccess)
+  if (preload_q8_cache_kernels() != cudaSuccess || preload_q8_attn_kernels() != cudaSuccess ||
+      preload_prefix_kernels() != cudaSuccess)
     return OASIS_ECUDA;
   if (cudaMemset(workspace, 0, 256) != cudaSuccess) return OASIS_ECUDA;
   oasis_q8* q = new (std::nothrow) oasis_q8;
@@ -229,6 +232,31 @@ int attn_args(oasis_q8* q8, const char* who, int R, int S, int causal, const voi
   return OASIS_OK;
 }
 
+// A map of a prefix [Hkv][blocks][2][B][d] with boxes of 8 blocks' keys or
+// values, 64 dims: 128 tokens of 128 bytes.  Blocks past the end read as 0.
+int prefix_map(oasis_q8* q8, const void* kv, int blocks, CUtensorMap* map) {
+  static const auto encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  if (!encode) return q8->fail(OASIS_ECUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[5] = {kHeadDim, kBlock, 2, static_cast<cuuint64_t>(blocks),
+                              static_cast<cuuint64_t>(q8->cfg.num_kv_heads)};
+  const cuuint64_t strides[4] = {kHeadDim * 2, kBlock * kHeadDim * 2, kUnitBytes,
+                                 static_cast<cuuint64_t>(blocks) * kUnitBytes};
+  const cuuint32_t box[5] = {64, kBlock, 1, 8, 1}, one[5] = {1, 1, 1, 1, 1};
+  if (encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(kv), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return q8->fail(OASIS_ECUDA, "prefix_attn: tensor map encode failed");
+  return OASIS_OK;
+}
+
 }  // namespace
 
 OASIS_API int oasis_q8_attn(oasis_q8* q8, int num_requests, int num_queries, int causal,
@@ -250,7 +278,9 @@ OASIS_API int oasis_prefix_workspace(const oasis_q8* q8, int num_requests, int n
   if (!q8 || !bytes || num_requests < 0 || num_requests > 65535 || num_queries < 1 ||
       num_queries > kQ8MaxQueries || prefix_len < 0)
     return OASIS_EINVAL;
-  *bytes = 0;
+  *bytes = num_requests > 0 && prefix_len > 0
+               ? prefix_shape(num_requests, num_queries, q8->G, q8->cfg.num_kv_heads, prefix_len).bytes
+               : 0;
   return OASIS_OK;
 }
 
@@ -275,11 +305,34 @@ OASIS_API int oasis_prefix_attn(oasis_q8* q8, int num_requests, int num_queries,
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
     return q8->fail(OASIS_EINVAL, "prefix_attn: workspace null, misaligned (256 bytes) or under %zu bytes", need);
   if (num_requests == 0) return OASIS_OK;
-  a.prefix = prefix_kv;
-  a.prefix_blocks = prefix_blocks;
-  a.prefix_len = prefix_len;
   OnDevice dev(q8->cfg.device);
   if (int rc = q8->cuda(dev.error(), "cudaSetDevice")) return rc;
+  if (prefix_len > 0) {
+    const PrefixShape sh = prefix_shape(num_requests, num_queries, q8->G, q8->cfg.num_kv_heads, prefix_len);
+    CUtensorMap map;
+    if (int rc = prefix_map(q8, prefix_kv, prefix_blocks, &map)) return rc;
+    PrefixArgs p{};
+    p.q = q;
+    p.part = static_cast<float*>(workspace);
+    p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + sh.part_bytes);
+    p.err = q8->err;
+    p.R = num_requests;
+    p.S = num_queries;
+    p.Hq = q8->cfg.num_q_heads;
+    p.Hkv = q8->cfg.num_kv_heads;
+    p.G = q8->G;
+    p.prefix_len = prefix_len;
+    p.row_tiles = sh.row_tiles;
+    p.splits = sh.splits;
+    p.scale_log2 = q8->scale_log2;
+    p.wait_limit = kWaitLimitCycles;
+    if (int rc = q8->cuda(launch_prefix(p, sh.tiles, map, static_cast<cudaStream_t>(stream)),
+                          "prefix_attn launch"))
+      return rc;
+    a.part = p.part;
+    a.stat = p.stat;
+    a.splits = sh.splits;
+  }
   return q8->cuda(launch_q8_attn(a, static_cast<cudaStream_t>(stream)), "prefix_attn launch");
 }
 

@@ -92,9 +92,22 @@ __device__ __forceinline__ void join_sum(float& m, float& l, float m2, float l2)
   l = l * scale_of(m, mx) + l2 * scale_of(m2, mx);
   m = mx;
 }
-// What queries see nothing of is 0.
-__device__ __forceinline__ float output(float acc, float m, float sum, float msum) {
-  return sum == 0.f ? 0.f : acc / sum * ex2(m - kWeightLog2 - msum);
+// The output of a query: `acc` in units of 2^(m - 14) and `sum` in units of
+// 2^msum of its own tokens, joined with what the shares of a prefix found
+// (element `at` of row `row`'s first share).  What it sees nothing of is 0.
+__device__ __forceinline__ float output(const Q8AttnArgs& a, float acc, float m, float sum, float msum,
+                                        int64_t row, int d) {
+  if (a.splits == 0) return sum == 0.f ? 0.f : acc / sum * ex2(m - kWeightLog2 - msum);
+  const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * a.S * a.G;
+  float all = sum, mall = msum;
+  for (int i = 0; i < a.splits; ++i) {
+    const float2 st = __ldg(a.stat + i * rows + row);
+    join_sum(mall, all, st.x, st.y);
+  }
+  float v = m == -INFINITY ? acc : acc * ex2(m - kWeightLog2 - mall);
+  for (int i = 0; i < a.splits; ++i)
+    v = fmaf(ex2(__ldg(a.stat + i * rows + row).x - mall), __ldg(a.part + (i * rows + row) * kHeadDim + d), v);
+  return v / all;
 }
 
 template <typename T, int W, int kNT>
@@ -474,8 +487,10 @@ __global__ void __launch_bounds__(W * 32)
     }
   }
   __syncthreads();
-  auto put = [&](int c, int d, float v) {
+  auto put = [&](int c, int d, float acc, float m, float sum, float msum) {
     const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
+    const float v = output(a, acc, m, sum, msum,
+                           (static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0 + c, d);
     const int64_t at = ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim + d;
     if (a.out_fp32) static_cast<float*>(a.out)[at] = v;
     else static_cast<T*>(a.out)[at] = static_cast<T>(v);
@@ -491,7 +506,7 @@ __global__ void __launch_bounds__(W * 32)
       join_sum(msum, sum, pml[w * kCols + c], pl[w * kCols + c]);
     }
     if (cluster == 1) {
-      put(c, d, output(acc, mx, sum, msum));
+      put(c, d, acc, mx, sum, msum);
     } else {
       merged[e] = acc;
       if (d == 0) {
@@ -511,93 +526,11 @@ __global__ void __launch_bounds__(W * 32)
       acc = fmaf(scale_of(load_remote(mm + c, i), mx), load_remote(merged + e, i), acc);
       join_sum(msum, sum, load_remote(mml + c, i), load_remote(ml + c, i));
     }
-    put(c, e % kHeadDim, output(acc, mx, sum, msum));
+    put(c, e % kHeadDim, acc, mx, sum, msum);
   }
   cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
-constexpr int kWarps = 4;
-
-// One CTA per query vector (query s of request r, head hq): each warp takes
-// every fourth token with a running maximum and sum; the four are joined in
-// shared memory.  A lane holds four dims.
-template <typename T>
-__global__ void simple_kernel(const Q8AttnArgs a) {
-  const int vec = blockIdx.x;  // ((s * R) + r) * Hq + hq
-  const int hq = vec % a.Hq, r = (vec / a.Hq) % a.R, s = vec / a.Hq / a.R;
-  const int h = hq / a.G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int len = max(a.len[r], 0);
-  if (len > a.max_blocks * kBlock) {
-    if (threadIdx.x == 0) raise_error(a.err, kErrBadBlock);
-    len = a.max_blocks * kBlock;
-  }
-  const int limit = max(a.causal ? len - (a.S - 1 - s) : len, 0);
-  float q[4];
-  const T* qp = static_cast<const T*>(a.q) + static_cast<int64_t>(vec) * kHeadDim + lane * 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = as_float(qp[i]) * a.scale_log2;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  auto token = [&](const float* k, const float* v) {
-    float x = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    const float mn = fmaxf(m, x);
-    const float al = mn == -INFINITY ? 1.f : exp2f(m - mn), p = mn == -INFINITY ? 0.f : exp2f(x - mn);
-    m = mn;
-    l = l * al + p;
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * al + p * v[i];
-  };
-  for (int t = warp; t < a.prefix_len; t += kWarps) {
-    const __nv_bfloat16* u = static_cast<const __nv_bfloat16*>(a.prefix) +
-        (static_cast<int64_t>(h) * a.prefix_blocks + t / kBlock) * kUnitElems + (t % kBlock) * kHeadDim + lane * 4;
-    float k[4], v[4];
-    for (int i = 0; i < 4; ++i) {
-      k[i] = __bfloat162float(u[i]);
-      v[i] = __bfloat162float(u[kBlock * kHeadDim + i]);
-    }
-    token(k, v);
-  }
-  for (int t = warp; t < limit; t += kWarps) {
-    const int page = a.table[static_cast<int64_t>(r) * a.max_blocks + t / kBlock];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) raise_error(a.err, kErrBadBlock);
-      continue;
-    }
-    const uint8_t* u = a.pages + (static_cast<int64_t>(page) * a.Hkv + h) * kQ8UnitBytes;
-    const int j = t % kBlock;
-    const float ks = pow2f(u[kQ8ExpOffset + j] - 127), vs = pow2f(u[kQ8ExpOffset + kBlock + j] - 127);
-    float k[4], v[4];
-    for (int i = 0; i < 4; ++i) {
-      k[i] = ks * __half2float(__ushort_as_half(q8_unpack2(u[q8_key_at(j, lane * 4 + i)])));
-      v[i] = vs * __half2float(__ushort_as_half(q8_unpack2(u[q8_value_at(j, lane * 4 + i)])));
-    }
-    token(k, v);
-  }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kHeadDim];
-  for (int i = 0; i < 4; ++i) so[warp][lane * 4 + i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  const int d = threadIdx.x;
-  float mx = -INFINITY, acc = 0.f, den = 0.f;
-  for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm[w]);
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - mx);
-    acc += f * so[w][d];
-    den += f * sl[w];
-  }
-  const float v = den == 0.f ? 0.f : acc / den;
-  const int64_t at = static_cast<int64_t>(vec) * kHeadDim + d;
-  if (a.out_fp32) static_cast<float*>(a.out)[at] = v;
-  else static_cast<T*>(a.out)[at] = static_cast<T>(v);
-}
-
-
-#ifndef Q8_W
-#define Q8_W 4
-#endif
-constexpr int kAttnWarps = Q8_W;
+constexpr int kAttnWarps = 4;
 
 template <typename T, int kNT>
 cudaError_t configure() {
@@ -646,21 +579,15 @@ cudaError_t launch_n(const Q8AttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s) {
   if (a.R == 0) return cudaSuccess;
-  if (a.prefix_len > 0) {
-    simple_kernel<__nv_bfloat16><<<static_cast<unsigned>(a.S) * a.R * a.Hq, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
-  }
   return a.type == kBf16 ? launch_n<__nv_bfloat16>(a, s) : launch_n<__half>(a, s);
 }
 
 // Their code and shared memory on the current device.
 cudaError_t preload_q8_attn_kernels() {
-  cudaFuncAttributes at;
   cudaError_t e = configure<__nv_bfloat16, 1>();
   if (e == cudaSuccess) e = configure<__nv_bfloat16, 2>();
   if (e == cudaSuccess) e = configure<__half, 1>();
   if (e == cudaSuccess) e = configure<__half, 2>();
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, simple_kernel<__nv_bfloat16>);
   return e;
 }
 
