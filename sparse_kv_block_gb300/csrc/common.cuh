@@ -165,6 +165,15 @@ __device__ __forceinline__ float load_remote(const float* p, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ float4 load_remote4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote_smem(p, rank))
+               : "memory");
+  return v;
+}
+
 // ------------------------------------------------------ warp-level matrix
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& a0,
                                         uint32_t& a1, uint32_t& a2,
@@ -244,6 +253,21 @@ __device__ __forceinline__ float f2sum(uint64_t v) {
 __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void f2unpack(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// The largest of three.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 

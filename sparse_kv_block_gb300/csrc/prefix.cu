@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   uint64_t* drain = o_done + 2;
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
 
+  asm volatile("griddepcontrol.launch_dependents;");  // the page attention may take idle SMs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_tile = blockIdx.x % a.row_tiles;
   const int h = (blockIdx.x / a.row_tiles) % a.Hkv;
@@ -285,8 +286,12 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      for (int c = 4; c < 124; c += 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmax3(mx[j], s[c + 2 * j], s[c + 2 * j + 1]);
+      mx[0] = fmax3(mx[0], s[124], s[125]);
+      mx[1] = fmax3(mx[1], s[126], s[127]);
+      const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sc;
       float alpha = 1.f;
       if (top > m + kLazy || m == -INFINITY) {
         const float to = fmaxf(top, m);
@@ -309,20 +314,23 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
       }
       l *= alpha;
       const float off = m == -INFINITY ? 0.f : -m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t sc2 = f2pack(sc, sc), off2 = f2pack(off, off);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float p0 = ex2(fmaf(s[c * 64 + 2 * j], sc, off)), p1 = ex2(fmaf(s[c * 64 + 2 * j + 1], sc, off));
-          sum[(2 * j) & 3] += p0;
-          sum[(2 * j + 1) & 3] += p1;
+          float p0, p1;
+          f2unpack(ffma2(f2pack(s[c * 64 + 2 * j], s[c * 64 + 2 * j + 1]), sc2, off2), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          sum[j & 1] = fadd2(sum[j & 1], f2pack(p0, p1));
           w[j] = pack_bf16x2(p0, p1);
         }
         tmem_st32(s_at + c * 32, w);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += f2sum(fadd2(sum[0], sum[1]));
       tmem_wait_st();
       fence_before();
       mbar_arrive(&p_full[t]);

@@ -92,22 +92,60 @@ __device__ __forceinline__ void join_sum(float& m, float& l, float m2, float l2)
   l = l * scale_of(m, mx) + l2 * scale_of(m2, mx);
   m = mx;
 }
-// The output of a query: `acc` in units of 2^(m - 14) and `sum` in units of
-// 2^msum of its own tokens, joined with what the shares of a prefix found
-// (element `at` of row `row`'s first share).  What it sees nothing of is 0.
-__device__ __forceinline__ float output(const Q8AttnArgs& a, float acc, float m, float sum, float msum,
-                                        int64_t row, int d) {
-  if (a.splits == 0) return sum == 0.f ? 0.f : acc / sum * ex2(m - kWeightLog2 - msum);
-  const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * a.S * a.G;
-  float all = sum, mall = msum;
-  for (int i = 0; i < a.splits; ++i) {
-    const float2 st = __ldg(a.stat + i * rows + row);
-    join_sum(mall, all, st.x, st.y);
+__device__ __forceinline__ void add4(float4& a, float f, const float4& x) {
+  a.x = fmaf(f, x.x, a.x);
+  a.y = fmaf(f, x.y, a.y);
+  a.z = fmaf(f, x.z, a.z);
+  a.w = fmaf(f, x.w, a.w);
+}
+
+// A warp's output of one query: four dims a lane, `acc` in units of
+// 2^(m - 14) and `sum` in units of 2^msum of the request's own tokens, joined
+// with what the shares of a prefix found (row `row` of each).  What the query
+// sees nothing of is 0.
+__device__ __forceinline__ float4 output(const Q8AttnArgs& a, float4 acc, float m, float sum, float msum,
+                                         int64_t row, int lane) {
+  float all = sum, f;
+  if (a.splits == 0) {
+    if (sum == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
+    f = ex2(m - kWeightLog2 - msum);
+  } else {
+    const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * a.S * a.G;
+    float mall = -INFINITY;
+    for (int i = lane; i < a.splits; i += 32) mall = fmaxf(mall, __ldcg(a.stat + i * rows + row).x);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) mall = fmaxf(mall, __shfl_xor_sync(0xffffffffu, mall, off));
+    mall = fmaxf(mall, msum);
+    f = m == -INFINITY ? 1.f : ex2(m - kWeightLog2 - mall);
+    const float own = f;
+    acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
+    all = 0.f;
+    for (int i0 = 0; i0 < a.splits; i0 += 32) {
+      float w = 0.f;
+      if (i0 + lane < a.splits) {
+        const float2 st = __ldcg(a.stat + (i0 + lane) * rows + row);
+        w = ex2(st.x - mall);
+        all = fmaf(w, st.y, all);
+      }
+      const int some = min(a.splits - i0, 32);
+      const float4* part = reinterpret_cast<const float4*>(a.part) + (i0 * rows + row) * 32 + lane;
+#pragma unroll 8
+      for (int i = 0; i < some; ++i) add4(acc, __shfl_sync(0xffffffffu, w, i), __ldcg(part + i * rows * 32));
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+    all = fmaf(sum, scale_of(msum, mall), all);
+    f = 1.f;
   }
-  float v = m == -INFINITY ? acc : acc * ex2(m - kWeightLog2 - mall);
-  for (int i = 0; i < a.splits; ++i)
-    v = fmaf(ex2(__ldg(a.stat + i * rows + row).x - mall), __ldg(a.part + (i * rows + row) * kHeadDim + d), v);
-  return v / all;
+  return make_float4(acc.x / all * f, acc.y / all * f, acc.z / all * f, acc.w / all * f);
+}
+
+__device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ void store4(__half* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
 }
 
 template <typename T, int W, int kNT>
@@ -487,29 +525,32 @@ __global__ void __launch_bounds__(W * 32)
     }
   }
   __syncthreads();
-  auto put = [&](int c, int d, float acc, float m, float sum, float msum) {
+  if (a.splits) asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's results
+  auto put = [&](int c, float4 acc, float m, float sum, float msum) {
     const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
-    const float v = output(a, acc, m, sum, msum,
-                           (static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0 + c, d);
-    const int64_t at = ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim + d;
-    if (a.out_fp32) static_cast<float*>(a.out)[at] = v;
-    else static_cast<T*>(a.out)[at] = static_cast<T>(v);
+    const float4 v = output(a, acc, m, sum, msum,
+                            (static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0 + c, lane);
+    const int64_t at = ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim + lane * 4;
+    if (a.out_fp32) store4(static_cast<float*>(a.out) + at, v);
+    else store4(static_cast<T*>(a.out) + at, v);
   };
-  for (int e = threadIdx.x; e < cols * kHeadDim; e += W * 32) {
-    const int c = e / kHeadDim, d = e % kHeadDim;
-    float mx = -INFINITY, msum = -INFINITY, acc = 0.f, sum = 0.f;
+  // A warp per column, four dims a lane.
+  for (int c = warp; c < cols; c += W) {
+    float mx = -INFINITY, msum = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) mx = fmaxf(mx, pm[w * kCols + c]);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      acc = fmaf(scale_of(pm[w * kCols + c], mx), part[(w * kCols + c) * kHeadDim + d], acc);
+      add4(acc, scale_of(pm[w * kCols + c], mx),
+           *reinterpret_cast<const float4*>(part + (w * kCols + c) * kHeadDim + lane * 4));
       join_sum(msum, sum, pml[w * kCols + c], pl[w * kCols + c]);
     }
     if (cluster == 1) {
-      put(c, d, acc, mx, sum, msum);
+      put(c, acc, mx, sum, msum);
     } else {
-      merged[e] = acc;
-      if (d == 0) {
+      *reinterpret_cast<float4*>(merged + c * kHeadDim + lane * 4) = acc;
+      if (lane == 0) {
         mm[c] = mx;
         mml[c] = msum;
         ml[c] = sum;
@@ -518,15 +559,15 @@ __global__ void __launch_bounds__(W * 32)
   }
   if (cluster == 1) return;
   cluster_sync();
-  for (int e = rank * W * 32 + threadIdx.x; e < cols * kHeadDim; e += cluster * W * 32) {
-    const int c = e / kHeadDim;
-    float mx = -INFINITY, msum = -INFINITY, acc = 0.f, sum = 0.f;
+  for (int c = rank * W + warp; c < cols; c += cluster * W) {
+    float mx = -INFINITY, msum = -INFINITY, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = 0; i < cluster; ++i) mx = fmaxf(mx, load_remote(mm + c, i));
     for (int i = 0; i < cluster; ++i) {
-      acc = fmaf(scale_of(load_remote(mm + c, i), mx), load_remote(merged + e, i), acc);
+      add4(acc, scale_of(load_remote(mm + c, i), mx), load_remote4(merged + c * kHeadDim + lane * 4, i));
       join_sum(msum, sum, load_remote(mml + c, i), load_remote(ml + c, i));
     }
-    put(c, e % kHeadDim, acc, mx, sum, msum);
+    put(c, acc, mx, sum, msum);
   }
   cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
@@ -559,12 +600,16 @@ cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   cfg.blockDim = dim3(kAttnWarps * 32);
   cfg.dynamicSmemBytes = Layout<kAttnWarps, kNT>::kBytes;
   cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  // Behind a prefix's launch: may start while that one still runs, and waits
+  // for its results before the last join.
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.splits ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, attn_kernel<T, kAttnWarps, kNT>, a, cluster);
 }
 
