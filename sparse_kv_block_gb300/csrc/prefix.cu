@@ -62,25 +62,31 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t at, uint32_t leading) {
 constexpr uint32_t kInstr = 1u << 4 | 1u << 7 | 1u << 10 | (128u >> 3) << 17 | (128u >> 4) << 24;
 constexpr uint32_t kInstrBt = kInstr | 1u << 16;
 
+// Called by a whole warp, issued by its elected lane: descriptors that are
+// the warp's alike stay in uniform registers, where the instruction wants
+// them.  (From a branch of one lane each product took 70 cycles to issue,
+// more than the 64 it runs.)
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(kInstr), "r"(add)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(kInstrBt), "r"(add)
       : "memory");
 }
-// Arrive on `bar` when this thread's products so far are done.
+// Arrive on `bar` when the elected lane's products so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_s;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_s, 0);
 
   bool ok = true;
   if (warp == kTiles * 4) {
@@ -208,47 +214,53 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
     }
   } else if (warp == kTiles * 4 + 1) {
     // ---- products
-    if (lane == 0) {
-      auto stage = [&](int j) { return smem_u32(smem + Lay::kRing + (j % kRingStages) * kStageBytes); };
-      auto landed = [&](int j) { return mbar_wait(&full[j % kRingStages], (j / kRingStages) & 1, a.wait_limit); };
-      auto scores = [&](int t, int i) {
-        const uint32_t q = smem_u32(smem + Lay::kQ + t * kStageBytes), k = stage(2 * i);
+    auto reached = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wait_limit)) != 0;
+    };
+    auto landed = [&](int j) { return reached(&full[j % kRingStages], (j / kRingStages) & 1); };
+    const uint64_t q_desc = smem_desc(smem_u32(smem + Lay::kQ), 16);
+    const uint64_t k_desc = smem_desc(smem_u32(smem + Lay::kRing), 16);
+    const uint64_t v_desc = smem_desc(smem_u32(smem + Lay::kRing), kHalfTile);
+    constexpr uint64_t kStep = kStageBytes >> 4;  // between tiles and stages, in a descriptor
+    auto scores = [&](int t, int i) {
+      const uint64_t q = q_desc + t * kStep, k = k_desc + (2 * i) % kRingStages * kStep;
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {  // 16 dims a step
-          const uint32_t off = (s >> 2) * kHalfTile + (s & 3) * 32;
-          mma_ss(tmem + t * 128, smem_desc(q + off, 16), smem_desc(k + off, 16), s > 0);
-        }
-        mma_commit(&s_full[t]);
-        if (t == kTiles - 1) mma_commit(&empty[(2 * i) % kRingStages]);
-      };
-      ok = landed(0);
-      if (ok) {
-        fence_after();
-        for (int t = 0; t < kTiles; ++t) scores(t, 0);
+      for (int s = 0; s < 8; ++s) {  // 16 dims a step
+        constexpr int kHalf = kHalfTile >> 4;
+        const uint32_t off = (s >> 2) * kHalf + (s & 3) * 2;
+        mma_ss(tmem + t * 128, q + off, k + off, s > 0);
       }
-      for (int i = 0; i < n && ok; ++i) {
-        ok = landed(2 * i + 1);
-        const uint32_t v = stage(2 * i + 1);
-        for (int t = 0; t < kTiles && ok; ++t) {
-          ok = mbar_wait(&p_full[t], i & 1, a.wait_limit);
-          if (!ok) break;
-          fence_after();
+      mma_commit(&s_full[t]);
+      if (t == kTiles - 1) mma_commit(&empty[(2 * i) % kRingStages]);
+    };
+    ok = landed(0);
+    if (ok) {
+      fence_after();
 #pragma unroll
-          for (int s = 0; s < 8; ++s)  // 16 tokens a step
-            mma_ts(tmem + kTiles * 128 + t * 128, tmem + t * 128 + s * 8, smem_desc(v + s * 16 * 128, kHalfTile),
-                   i > 0 || s > 0);
-          mma_commit(&o_done[t]);
-          if (t == kTiles - 1) mma_commit(&empty[(2 * i + 1) % kRingStages]);
-          if (i + 1 < n) {
-            if (t == 0) ok = landed(2 * i + 2);
-            if (!ok) break;
-            scores(t, i + 1);
-          }
-        }
-      }
-      mma_commit(drain);
-      (void)mbar_wait(drain, 0);
+      for (int t = 0; t < kTiles; ++t) scores(t, 0);
     }
+    for (int i = 0; i < n && ok; ++i) {
+      ok = landed(2 * i + 1);
+      const uint64_t v = v_desc + (2 * i + 1) % kRingStages * kStep;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        ok = ok && reached(&p_full[t], i & 1);
+        if (!ok) break;
+        fence_after();
+#pragma unroll
+        for (int s = 0; s < 8; ++s)  // 16 tokens a step
+          mma_ts(tmem + kTiles * 128 + t * 128, tmem + t * 128 + s * 8, v + s * (16 * 128 >> 4), i > 0 || s > 0);
+        mma_commit(&o_done[t]);
+        if (t == kTiles - 1) mma_commit(&empty[(2 * i + 1) % kRingStages]);
+        if (i + 1 < n) {
+          if (t == 0) ok = landed(2 * i + 2);
+          if (!ok) break;
+          scores(t, i + 1);
+        }
+      }
+    }
+    mma_commit(drain);
+    (void)reached(drain, 0);
   } else {
     // ---- softmax of row `lane` of this warp's quarter of tile t
     const int t = warp >> 2;
