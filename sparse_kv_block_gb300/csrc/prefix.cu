@@ -137,6 +137,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 32 bytes, a whole sector.
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 template <int kTiles>
 __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
     prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap map) {
@@ -147,7 +154,8 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   uint64_t* full = bars;                       // [4] a stage has landed
   uint64_t* empty = bars + kRingStages;        // [4] its products are done
   uint64_t* s_full = bars + 2 * kRingStages;   // [2] scores of a tile
-  uint64_t* p_full = s_full + 2;               // [2] its weights (128 threads)
+  uint64_t* p_half = s_full + 2;               // [2] its first 64 tokens' weights (128 threads)
+  uint64_t* p_full = p_half + 2;               // [2] all its weights
   uint64_t* o_done = p_full + 2;               // [2] its outputs
   uint64_t* drain = o_done + 2;
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
@@ -165,26 +173,41 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   const int n = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / a.splits) - tile0;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * kRingStages + 2; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&p_full[i], 128);
+    for (int i = 0; i < 2 * kRingStages + 2; ++i) mbar_init(&bars[i], 1);  // to s_full
+    for (int i = 0; i < 4; ++i) mbar_init(&p_half[i], 128);
     for (int i = 0; i < 2; ++i) mbar_init(&o_done[i], 1);
     mbar_init(drain, 1);
     fence_barrier_init();
     prefetch_tensormap(&map);
   }
   if (warp == kTiles * 4 + 1) tmem_alloc(tmem_s, Lay::kColumns);
-  // The query rows, 16 bytes a step, as the swizzle places them.
-  for (int e = threadIdx.x; e < kTiles * kTile * 16; e += Lay::kThreads) {
-    const int rr = e >> 4, ch = e & 15, row = row0 + rr;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row < rows) {
-      const int r = row / per_request, c = row % per_request;
-      v = __ldg(reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(a.q) +
-          ((static_cast<int64_t>(c / a.G) * a.R + r) * a.Hq + h * a.G + c % a.G) * kHeadDim + ch * 8));
+  // The query rows, half a warp a row, as the swizzle places them; a few rows
+  // at a time so that their loads are in flight together.
+  {
+    constexpr int kBatch = 8, kStep = Lay::kThreads / 16;
+    const int ch = threadIdx.x & 15;
+    for (int r0 = threadIdx.x >> 4; r0 < kTiles * kTile; r0 += kBatch * kStep) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int rr = r0 + b * kStep, row = row0 + rr;
+        v[b] = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < kTiles * kTile && row < rows) {
+          const int r = row / per_request, c = row - r * per_request, s = c / a.G;
+          v[b] = __ldg(reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(a.q) +
+              ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + c - s * a.G) * kHeadDim + ch * 8));
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int rr = r0 + b * kStep;
+        if (rr < kTiles * kTile) {
+          uint8_t* tile = smem + Lay::kQ + (rr / kTile) * kStageBytes + (ch >> 3) * kHalfTile;
+          *reinterpret_cast<uint4*>(tile + (rr % kTile) * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[b];
+        }
+      }
     }
-    uint8_t* tile = smem + Lay::kQ + (rr / kTile) * kStageBytes + (ch >> 3) * kHalfTile;
-    *reinterpret_cast<uint4*>(tile + (rr % kTile) * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   fence_before();
@@ -244,12 +267,16 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
       const uint64_t v = v_desc + (2 * i + 1) % kRingStages * kStep;
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        ok = ok && reached(&p_full[t], i & 1);
-        if (!ok) break;
-        fence_after();
 #pragma unroll
-        for (int s = 0; s < 8; ++s)  // 16 tokens a step
-          mma_ts(tmem + kTiles * 128 + t * 128, tmem + t * 128 + s * 8, v + s * (16 * 128 >> 4), i > 0 || s > 0);
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && reached(half ? &p_full[t] : &p_half[t], i & 1);
+          if (!ok) break;
+          fence_after();
+#pragma unroll
+          for (int s = half * 4; s < half * 4 + 4; ++s)  // 16 tokens a step
+            mma_ts(tmem + kTiles * 128 + t * 128, tmem + t * 128 + s * 8, v + s * (16 * 128 >> 4), i > 0 || s > 0);
+        }
+        if (!ok) break;
         mma_commit(&o_done[t]);
         if (t == kTiles - 1) mma_commit(&empty[(2 * i + 1) % kRingStages]);
         if (i + 1 < n) {
@@ -341,11 +368,11 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
           w[j] = pack_bf16x2(p0, p1);
         }
         tmem_st32(s_at + c * 32, w);
+        tmem_wait_st();
+        fence_before();
+        mbar_arrive(c ? &p_full[t] : &p_half[t]);
       }
       l += f2sum(fadd2(sum[0], sum[1]));
-      tmem_wait_st();
-      fence_before();
-      mbar_arrive(&p_full[t]);
     }
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (n - 1) & 1, a.wait_limit));
     if (ok) {
@@ -358,9 +385,9 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
         tmem_ld32(o_at + c * 32, o);
         tmem_wait_ld();
         if (row < rows) {
-          float4* dst = reinterpret_cast<float4*>(a.part + at * kHeadDim + c * 32);
+          float* dst = a.part + at * kHeadDim + c * 32;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < 4; ++j) store8(dst + j * 8, o + j * 8);
         }
       }
       if (row < rows) a.stat[at] = make_float2(m, l);
