@@ -681,7 +681,8 @@ OASIS_API int oasis_q8_write(oasis_q8* q8, const void* k, const void* v, int typ
  * `type`, the units of oasis_dense_attn's cache, of a host store and of
  * oasis_prefix_attn's prefix.  Exact in bf16 and fp32 (rounded in fp16).
  * Tokens at or past seq_len (and those of a bad page) are left as they are.
- * out 16-byte aligned. */
+ * out 16-byte aligned, out_blocks >= 1; a length past 16 * min(out_blocks,
+ * max_blocks) raises BAD_BLOCK_ID and what fits is written. */
 OASIS_API int oasis_q8_read(oasis_q8* q8, int num_requests, const int32_t* page_table,
                             const int32_t* seq_len, void* out, int type, int out_blocks,
                             void* stream);

@@ -172,13 +172,27 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * split / a.splits);
   const int n = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / a.splits) - tile0;
 
-  if (threadIdx.x == 0) {
+  // The loading thread sets the barriers up and starts at once: the first
+  // tiles come in while the queries are placed.  Stage 2 i is tile i's keys,
+  // 2 i + 1 its values.
+  const bool loader = threadIdx.x == kTiles * 128;
+  auto load = [&](int j) {
+    const int st = j % kRingStages;
+    uint8_t* dst = smem + Lay::kRing + st * kStageBytes;
+    const int block = (tile0 + (j >> 1)) * (kTile / kBlock);
+    mbar_arrive_expect_tx(&full[st], kStageBytes);
+    load_blocks(dst, &map, 0, j & 1, block, h, &full[st]);
+    load_blocks(dst + kHalfTile, &map, 64, j & 1, block, h, &full[st]);
+  };
+  int loaded = 0;
+  if (loader) {
+    prefetch_tensormap(&map);
     for (int i = 0; i < 2 * kRingStages + 2; ++i) mbar_init(&bars[i], 1);  // to s_full
     for (int i = 0; i < 4; ++i) mbar_init(&p_half[i], 128);
     for (int i = 0; i < 2; ++i) mbar_init(&o_done[i], 1);
     mbar_init(drain, 1);
     fence_barrier_init();
-    prefetch_tensormap(&map);
+    for (; loaded < 2 * n && loaded < kRingStages; ++loaded) load(loaded);
   }
   if (warp == kTiles * 4 + 1) tmem_alloc(tmem_s, Lay::kColumns);
   // The query rows, half a warp a row, as the swizzle places them; a few rows
@@ -217,19 +231,13 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
 
   bool ok = true;
   if (warp == kTiles * 4) {
-    // ---- loads: stage 2 i is tile i's keys, 2 i + 1 its values
-    if (lane == 0) {
-      int loaded = 0;
-      for (int j = 0; j < 2 * n && ok; ++j) {
-        const int st = j % kRingStages;
-        if (j >= kRingStages) ok = mbar_wait(&empty[st], (j / kRingStages - 1) & 1, a.wait_limit);
+    // ---- loads
+    if (loader) {
+      for (; loaded < 2 * n && ok; ++loaded) {
+        const int st = loaded % kRingStages;
+        ok = mbar_wait(&empty[st], (loaded / kRingStages - 1) & 1, a.wait_limit);
         if (!ok) break;
-        uint8_t* dst = smem + Lay::kRing + st * kStageBytes;
-        const int block = (tile0 + (j >> 1)) * (kTile / kBlock);
-        mbar_arrive_expect_tx(&full[st], kStageBytes);
-        load_blocks(dst, &map, 0, j & 1, block, h, &full[st]);
-        load_blocks(dst + kHalfTile, &map, 64, j & 1, block, h, &full[st]);
-        loaded = j + 1;
+        load(loaded);
       }
       // No copy may outlive the CTA, whatever the other warps met.
       for (int j = max(loaded - kRingStages, 0); j < loaded; ++j)

@@ -41,108 +41,248 @@ __device__ __forceinline__ uint32_t quantise_row(float4 x, int& e) {
   return q8_pack4(x.x * s, x.y * s, x.z * s, x.w * s);
 }
 
-// One warp per (token, KV head).
-template <typename T>
-__global__ void write_kernel(const Q8WriteArgs a) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+// Four words of four bytes, transposed: byte i of word j to byte j of word i.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[0], w[1], 0x7362);
+  const uint32_t c = __byte_perm(w[2], w[3], 0x5140), d = __byte_perm(w[2], w[3], 0x7362);
+  w[0] = __byte_perm(a, c, 0x5410);
+  w[1] = __byte_perm(a, c, 0x7632);
+  w[2] = __byte_perm(b, d, 0x5410);
+  w[3] = __byte_perm(b, d, 0x7632);
+}
+
+// 32 bytes, a whole sector.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Rounding into the pages.  Bound by memory: 256 values are read and 258
+// bytes written a token and head.
+//
+// Values are stored with a block's tokens consecutive, so single tokens mean
+// single bytes 16 apart; whole blocks are worth finding.  The tokens are cut
+// into runs: a run begins where the slot is not the one before plus one, or
+// is a block's first, and so holds at most a block.  A warp takes kSpan
+// tokens' places, one head and keys or values, and treats every run that
+// begins there, reading on past its span where the run does; a run that is a
+// whole block is transposed in registers and stored in whole sectors.
+template <typename T, int kSpan>
+__global__ void __launch_bounds__(256) write_kernel(const Q8WriteArgs a) {
+  static_assert(kSpan <= kBlock, "a run from the span's last place ends within 32 lanes");
   const int lane = threadIdx.x & 31;
-  if (row >= static_cast<int64_t>(a.T) * a.Hkv) return;
-  const int t = static_cast<int>(row / a.Hkv), h = static_cast<int>(row - static_cast<int64_t>(t) * a.Hkv);
-  const int64_t slot = a.slots[t];
-  if (slot < 0) return;
-  if (slot >= a.num_slots) {
-    if (lane == 0) raise_error(a.err, kErrBadUnit);
-    return;
-  }
-  const int j = static_cast<int>(slot & (kBlock - 1));
-  uint8_t* unit = a.pages + ((slot >> 4) * a.Hkv + h) * static_cast<int64_t>(kQ8UnitBytes);
-  int ke, ve;
-  const uint32_t kc = quantise_row(
-      load4(static_cast<const T*>(a.k) + t * a.k_stride + h * kHeadDim + lane * 4), ke);
-  const uint32_t vc = quantise_row(
-      load4(static_cast<const T*>(a.v) + t * a.v_stride + h * kHeadDim + lane * 4), ve);
-  *reinterpret_cast<uint32_t*>(unit + q8_key_at(j, lane * 4)) = kc;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t spans = (static_cast<int64_t>(a.T) + kSpan - 1) / kSpan;
+  if (item >= spans * a.Hkv * 2) return;
+  const bool values = item & 1;
+  const int h = static_cast<int>((item >> 1) % a.Hkv);
+  const int t0 = static_cast<int>((item >> 1) / a.Hkv) * kSpan;
+  // Lane i holds the slot of token t0 + i (the span and a run's rest behind
+  // it); past the last token nothing continues a run.
+  const int64_t slot = lane < a.T - t0 ? a.slots[static_cast<int64_t>(t0) + lane] : -1;
+  int64_t before = __shfl_up_sync(0xffffffffu, slot, 1);
+  if (lane == 0) before = t0 > 0 ? a.slots[t0 - 1] : -2;
+  const bool begins = slot >= 0 && (slot != before + 1 || before < 0 || (slot & (kBlock - 1)) == 0);
+  const bool ends = slot < 0 || begins;  // the run before ends here
+  const unsigned ending = __ballot_sync(0xffffffffu, ends);
+  unsigned todo = __ballot_sync(0xffffffffu, begins && lane < kSpan);
+  const int64_t stride = values ? a.v_stride : a.k_stride;
+  const T* src = static_cast<const T*>(values ? a.v : a.k) + h * kHeadDim + lane * 4;
+  for (; todo; todo &= todo - 1) {
+    const int at = __ffs(todo) - 1;
+    const int64_t first = __shfl_sync(0xffffffffu, slot, at);
+    if (first >= a.num_slots) {
+      if (lane == 0) raise_error(a.err, kErrBadUnit);
+      continue;
+    }
+    // at + 16 <= 31: the token after a whole block begins a run in some lane.
+    const int n = __ffs(ending >> (at + 1));
+    const int j0 = static_cast<int>(first & (kBlock - 1));
+    uint8_t* unit = a.pages + ((first >> 4) * a.Hkv + h) * static_cast<int64_t>(kQ8UnitBytes);
+    const T* x = src + static_cast<int64_t>(t0 + at) * stride;
+    uint32_t codes[kBlock];
+    int mine = 0;  // exponent of token `lane` of the run
+    if (n == kBlock) {
+      float4 v[kBlock];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    unit[q8_value_at(j, lane * 4 + i)] = static_cast<uint8_t>(vc >> (8 * i));
-  if (lane == 0) {
-    unit[kQ8ExpOffset + j] = static_cast<uint8_t>(ke + 127);
-    unit[kQ8ExpOffset + kBlock + j] = static_cast<uint8_t>(ve + 127);
+      for (int i = 0; i < kBlock; ++i) v[i] = load4(x + i * stride);
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) {
+        int e;
+        codes[i] = quantise_row(v[i], e);
+        if (lane == i) mine = e;
+      }
+      if (values) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4] = {codes[4 * q], codes[4 * q + 1], codes[4 * q + 2], codes[4 * q + 3]};
+          transpose4(w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) codes[4 * q + i] = w[i];
+        }
+        // codes[4 q + i]: tokens 4 q .. + 3 of dim 4 lane + i
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const uint32_t two[8] = {codes[i], codes[4 + i], codes[8 + i], codes[12 + i],
+                                   codes[i + 1], codes[5 + i], codes[9 + i], codes[13 + i]};
+          store32(unit + q8_value_at(0, lane * 4 + i), two);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i)
+          *reinterpret_cast<uint32_t*>(unit + q8_key_at(i, lane * 4)) = codes[i];
+      }
+    } else {
+      for (int i = 0; i < n; ++i) {
+        int e;
+        const uint32_t c = quantise_row(load4(x + i * stride), e);
+        if (lane == i) mine = e;
+        if (values) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            unit[q8_value_at(j0 + i, lane * 4 + d)] = static_cast<uint8_t>(c >> (8 * d));
+        } else {
+          *reinterpret_cast<uint32_t*>(unit + q8_key_at(j0 + i, lane * 4)) = c;
+        }
+      }
+    }
+    if (lane < n) unit[kQ8ExpOffset + (values ? kBlock : 0) + j0 + lane] = static_cast<uint8_t>(mine + 127);
   }
 }
 
-__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void store1(__half* p, float x) { *p = __float2half_rn(x); }
-
-__device__ __forceinline__ float q8_value(uint8_t code, uint8_t exp) {
-  const uint32_t h2 = q8_unpack2(code);
-  return __half2float(__ushort_as_half(static_cast<uint16_t>(h2))) * pow2f(exp - 127);
+// Two codes times a power of two, as two values of the output's type.
+__device__ __forceinline__ float2 values2(uint32_t codes, float s) {
+  const uint32_t h = q8_unpack2(codes);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return make_float2(f.x * s, f.y * s);
+}
+__device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float2 f) { return pack_bf16x2(f.x, f.y); }
+__device__ __forceinline__ uint32_t pack2(const __half*, float2 f) {
+  const __half2 v = __floats2half2_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// One CTA per (request, block): every KV head's unit.
+// Four codes of a row and its scale -> four values at p.
 template <typename T>
-__global__ void read_kernel(const Q8ReadArgs a) {
-  const int r = blockIdx.y, b = blockIdx.x;
+__device__ __forceinline__ void put4(T* p, uint32_t codes, float s) {
+  const float2 a = values2(codes & 0xffffu, s), b = values2(codes >> 16, s);
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(p, a), pack2(p, b));
+  }
+}
+
+// Reading back: a warp per unit, whose 4128 bytes are asked for at once; a
+// token's row of 128 values is then four values a lane (values are transposed
+// in registers).  Bound by memory, mostly by what it writes.
+template <typename T>
+__global__ void __launch_bounds__(256) read_kernel(const Q8ReadArgs a, int blocks) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (item >= static_cast<int64_t>(a.R) * blocks * a.Hkv) return;
+  const int h = static_cast<int>(item % a.Hkv);
+  const int b = static_cast<int>(item / a.Hkv % blocks);
+  const int r = static_cast<int>(item / a.Hkv / blocks);
   const int len = a.len[r];
-  const int n = len - b * kBlock;
-  if (n <= 0) return;
-  if (b == 0 && threadIdx.x == 0 && (len - 1) / kBlock >= min(a.max_blocks, a.out_blocks))
-    raise_error(a.err, kErrBadBlock);
-  if (b >= a.out_blocks) return;
   const int page = a.table[static_cast<int64_t>(r) * a.max_blocks + b];
+  const int valid = min(len - b * kBlock, kBlock);
+  if (b == 0 && h == 0 && lane == 0 && len > 0 && (len - 1) / kBlock >= blocks) raise_error(a.err, kErrBadBlock);
+  if (valid <= 0) return;
   if (page < 0 || page >= a.num_pages) {
-    if (threadIdx.x == 0) raise_error(a.err, kErrBadBlock);
+    if (lane == 0) raise_error(a.err, kErrBadBlock);
     return;
   }
-  const int valid = min(n, kBlock);
-  for (int h = 0; h < a.Hkv; ++h) {
-    const uint8_t* unit = a.pages + (static_cast<int64_t>(page) * a.Hkv + h) * kQ8UnitBytes;
-    T* out = static_cast<T*>(a.out) +
-             ((static_cast<int64_t>(r) * a.Hkv + h) * a.out_blocks + b) * kUnitElems;
-    for (int x = threadIdx.x; x < valid * kHeadDim; x += blockDim.x) {
-      const int j = x / kHeadDim, i = x % kHeadDim;
-      store1(out + x, q8_value(unit[q8_key_at(j, i)], unit[kQ8ExpOffset + j]));
-      store1(out + kBlock * kHeadDim + x,
-             q8_value(unit[q8_value_at(j, i)], unit[kQ8ExpOffset + kBlock + j]));
+  const uint8_t* unit = a.pages + (static_cast<int64_t>(page) * a.Hkv + h) * kQ8UnitBytes;
+  T* out = static_cast<T*>(a.out) + ((static_cast<int64_t>(r) * a.Hkv + h) * a.out_blocks + b) * kUnitElems +
+           lane * 4;
+  uint32_t k[kBlock], v[kBlock];
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j) k[j] = __ldg(reinterpret_cast<const uint32_t*>(unit + q8_key_at(j, lane * 4)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(unit + q8_value_at(0, lane * 4 + i)));
+    v[i] = w.x;
+    v[4 + i] = w.y;
+    v[8 + i] = w.z;
+    v[12 + i] = w.w;
+  }
+  const float scale = pow2f(__ldg(unit + kQ8ExpOffset + lane) - 127);  // lane: key, then value exponents
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    transpose4(w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * q + i] = w[i];
+  }
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j) {
+    const float ks = __shfl_sync(0xffffffffu, scale, j), vs = __shfl_sync(0xffffffffu, scale, kBlock + j);
+    if (j < valid) {
+      put4(out + j * kHeadDim, k[j], ks);
+      put4(out + (kBlock + j) * kHeadDim, v[j], vs);
     }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_q8_write(const Q8WriteArgs& a, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(a.T) * a.Hkv;
-  if (rows == 0) return cudaSuccess;
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-  if (a.type == kBf16) write_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  else if (a.type == kFp16) write_kernel<__half><<<grid, 256, 0, s>>>(a);
-  else write_kernel<float><<<grid, 256, 0, s>>>(a);
+namespace {
+
+constexpr int kLongSpan = 16;
+
+template <typename T>
+cudaError_t launch_write(const Q8WriteArgs& a, cudaStream_t s) {
+  // A span of 16 tokens a warp, or of one where that leaves SMs without work
+  // (a decode step's tokens, each in a page of its own).
+  const int64_t rows = static_cast<int64_t>(a.T) * a.Hkv * 2;
+  const bool one = rows < 152 * 64;
+  const int64_t items = one ? rows : (static_cast<int64_t>(a.T) + kLongSpan - 1) / kLongSpan * a.Hkv * 2;
+  const unsigned grid = static_cast<unsigned>((items + 7) / 8);
+  if (one) write_kernel<T, 1><<<grid, 256, 0, s>>>(a);
+  else write_kernel<T, kLongSpan><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_read(const Q8ReadArgs& a, cudaStream_t s) {
+  const int blocks = a.max_blocks < a.out_blocks ? a.max_blocks : a.out_blocks;
+  const int64_t items = static_cast<int64_t>(a.R) * blocks * a.Hkv;
+  if (items == 0) return cudaSuccess;
+  read_kernel<T><<<static_cast<unsigned>((items + 7) / 8), 256, 0, s>>>(a, blocks);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t preload() {
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, write_kernel<T, 1>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, write_kernel<T, kLongSpan>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, read_kernel<T>);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_q8_write(const Q8WriteArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  if (a.type == kBf16) return launch_write<__nv_bfloat16>(a, s);
+  if (a.type == kFp16) return launch_write<__half>(a, s);
+  return launch_write<float>(a, s);
 }
 
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
-  if (a.R == 0) return cudaSuccess;
-  const dim3 grid(a.max_blocks, a.R);
-  if (a.type == kBf16) read_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  else if (a.type == kFp16) read_kernel<__half><<<grid, 256, 0, s>>>(a);
-  else read_kernel<float><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.type == kBf16) return launch_read<__nv_bfloat16>(a, s);
+  if (a.type == kFp16) return launch_read<__half>(a, s);
+  return launch_read<float>(a, s);
 }
 
 cudaError_t preload_q8_cache_kernels() {
-  cudaFuncAttributes at;
-  const void* fns[] = {reinterpret_cast<const void*>(write_kernel<__nv_bfloat16>),
-                       reinterpret_cast<const void*>(write_kernel<__half>),
-                       reinterpret_cast<const void*>(write_kernel<float>),
-                       reinterpret_cast<const void*>(read_kernel<__nv_bfloat16>),
-                       reinterpret_cast<const void*>(read_kernel<__half>),
-                       reinterpret_cast<const void*>(read_kernel<float>)};
-  for (const void* f : fns) {
-    const cudaError_t e = cudaFuncGetAttributes(&at, f);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  cudaError_t e = preload<__nv_bfloat16>();
+  if (e == cudaSuccess) e = preload<__half>();
+  if (e == cudaSuccess) e = preload<float>();
+  return e;
 }
 
 }  // namespace oasis

@@ -143,6 +143,8 @@ OASIS_API int oasis_q8_write(oasis_q8* q8, const void* k, const void* v, int typ
   if (!q8) return OASIS_EINVAL;
   if (!any_type(type)) return q8->fail(OASIS_EINVAL, "q8_write: bad type %d", type);
   if (num_tokens < 0) return q8->fail(OASIS_EINVAL, "q8_write: num_tokens must be >= 0");
+  if (static_cast<int64_t>(num_tokens) * q8->cfg.num_kv_heads > (1ll << 33))
+    return q8->fail(OASIS_EINVAL, "q8_write: num_tokens * num_kv_heads must be <= 2^33");
   if (num_tokens == 0) return OASIS_OK;
   if (!k || !v || !slots) return q8->fail(OASIS_EINVAL, "q8_write: null pointer");
   const int b = type_bytes(type);
@@ -173,7 +175,10 @@ OASIS_API int oasis_q8_read(oasis_q8* q8, int num_requests, const int32_t* page_
   if (!any_type(type)) return q8->fail(OASIS_EINVAL, "q8_read: bad type %d", type);
   if (num_requests < 0 || num_requests > 65535)
     return q8->fail(OASIS_EINVAL, "q8_read: num_requests must be in 0..65535");
-  if (out_blocks < 0) return q8->fail(OASIS_EINVAL, "q8_read: out_blocks must be >= 0");
+  if (out_blocks < 1) return q8->fail(OASIS_EINVAL, "q8_read: out_blocks must be >= 1");
+  const int blocks = out_blocks < q8->cfg.max_blocks ? out_blocks : q8->cfg.max_blocks;
+  if (static_cast<int64_t>(num_requests) * blocks * q8->cfg.num_kv_heads > (1ll << 33))
+    return q8->fail(OASIS_EINVAL, "q8_read: num_requests * blocks * num_kv_heads must be <= 2^33");
   if (num_requests == 0) return OASIS_OK;
   if (!page_table || !seq_len || !out) return q8->fail(OASIS_EINVAL, "q8_read: null pointer");
   if (!aligned(out, 16) || !aligned(page_table, 4) || !aligned(seq_len, 4))

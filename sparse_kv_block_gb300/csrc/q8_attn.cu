@@ -92,52 +92,17 @@ __device__ __forceinline__ void join_sum(float& m, float& l, float m2, float l2)
   l = l * scale_of(m, mx) + l2 * scale_of(m2, mx);
   m = mx;
 }
+__device__ __forceinline__ void scale4(float4& a, float f) {
+  a.x *= f;
+  a.y *= f;
+  a.z *= f;
+  a.w *= f;
+}
 __device__ __forceinline__ void add4(float4& a, float f, const float4& x) {
   a.x = fmaf(f, x.x, a.x);
   a.y = fmaf(f, x.y, a.y);
   a.z = fmaf(f, x.z, a.z);
   a.w = fmaf(f, x.w, a.w);
-}
-
-// A warp's output of one query: four dims a lane, `acc` in units of
-// 2^(m - 14) and `sum` in units of 2^msum of the request's own tokens, joined
-// with what the shares of a prefix found (row `row` of each).  What the query
-// sees nothing of is 0.
-__device__ __forceinline__ float4 output(const Q8AttnArgs& a, float4 acc, float m, float sum, float msum,
-                                         int64_t row, int lane) {
-  float all = sum, f;
-  if (a.splits == 0) {
-    if (sum == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
-    f = ex2(m - kWeightLog2 - msum);
-  } else {
-    const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * a.S * a.G;
-    float mall = -INFINITY;
-    for (int i = lane; i < a.splits; i += 32) mall = fmaxf(mall, __ldcg(a.stat + i * rows + row).x);
-#pragma unroll
-    for (int off = 16; off; off >>= 1) mall = fmaxf(mall, __shfl_xor_sync(0xffffffffu, mall, off));
-    mall = fmaxf(mall, msum);
-    f = m == -INFINITY ? 1.f : ex2(m - kWeightLog2 - mall);
-    const float own = f;
-    acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
-    all = 0.f;
-    for (int i0 = 0; i0 < a.splits; i0 += 32) {
-      float w = 0.f;
-      if (i0 + lane < a.splits) {
-        const float2 st = __ldcg(a.stat + (i0 + lane) * rows + row);
-        w = ex2(st.x - mall);
-        all = fmaf(w, st.y, all);
-      }
-      const int some = min(a.splits - i0, 32);
-      const float4* part = reinterpret_cast<const float4*>(a.part) + (i0 * rows + row) * 32 + lane;
-#pragma unroll 8
-      for (int i = 0; i < some; ++i) add4(acc, __shfl_sync(0xffffffffu, w, i), __ldcg(part + i * rows * 32));
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-    all = fmaf(sum, scale_of(msum, mall), all);
-    f = 1.f;
-  }
-  return make_float4(acc.x / all * f, acc.y / all * f, acc.z / all * f, acc.w / all * f);
 }
 
 __device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
@@ -149,7 +114,7 @@ __device__ __forceinline__ void store4(__half* p, const float4& v) {
 }
 
 template <typename T, int W, int kNT>
-__global__ void __launch_bounds__(W * 32)
+__global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory allows
     attn_kernel(const Q8AttnArgs a, int cluster) {
   using Lay = Layout<W, kNT>;
   constexpr int kCols = Lay::kCols;
@@ -173,24 +138,42 @@ __global__ void __launch_bounds__(W * 32)
   }
   __syncwarp();
 
-  int len = max(a.len[r], 0);
+  // Loads that need nothing else, in flight together: the length, the first
+  // group's pages (rows of the table are readable throughout) and the queries.
+  const int first = rank * W + warp, step = cluster * W;
+  const int32_t* row = a.table + static_cast<int64_t>(r) * a.max_blocks;
+  auto page_of = [&](int k) {
+    const int64_t b = (first + static_cast<int64_t>(k) * step) * kGroupUnits + lane;
+    return lane < kGroupUnits && b < a.max_blocks ? __ldg(row + b) : -1;
+  };
+  int len = __ldg(a.len + r);
+  int page = page_of(0);
+  uint4 qv[kNT][4];  // of column g of a tile: dims 64 (j / 2) + 16 t + 8 (j % 2) .. + 7
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+    const int c = col0 + nt * 8 + g;
+    if (nt * 8 + g < cols) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const T*>(a.q) +
+          ((static_cast<int64_t>(c / a.G) * a.R + r) * a.Hq + h * a.G + c % a.G) * kHeadDim);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qv[nt][j] = __ldg(src + (j >> 1) * 8 + t * 2 + (j & 1));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qv[nt][j] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  len = max(len, 0);
   if (len > a.max_blocks * kBlock) {
     if (threadIdx.x == 0) raise_error(a.err, kErrBadBlock);
     len = a.max_blocks * kBlock;
   }
   const int groups = (len + kGroupTokens - 1) / kGroupTokens;
-  const int first = rank * W + warp, step = cluster * W;
   const int count = groups > first ? (groups - first + step - 1) / step : 0;
 
   // Lanes 0..3 fetch a group's pages (the table's entries a turn ahead) and
   // issue its copies: the keys as soon as the last group's have been used, so
   // that they come in beside its second half; then the values and exponents.
-  const int32_t* row = a.table + static_cast<int64_t>(r) * a.max_blocks;
-  auto page_of = [&](int k) {
-    const int b = (first + k * step) * kGroupUnits + lane;
-    return lane < kGroupUnits && k < count && b * kBlock < len ? __ldg(row + b) : -1;
-  };
-  int page = page_of(0);
   const uint8_t* src = nullptr;  // this lane's unit of the group issued last, if it has one
   auto issue_keys = [&](int k) {
     const int b = (first + k * step) * kGroupUnits + lane;
@@ -224,29 +207,18 @@ __global__ void __launch_bounds__(W * 32)
   int lim0[kNT], lim1[kNT];      // tokens those columns see
 #pragma unroll
   for (int nt = 0; nt < kNT; ++nt) {
-    const int c = nt * 8 + g;
     float x[32];
     float amax = 0.f;
-    if (c < cols) {
-      const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const T*>(a.q) +
-          ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // dims 64 (j / 2) + 16 t + 8 (j % 2) .. + 7
-        const uint4 v = __ldg(src + (j >> 1) * 8 + t * 2 + (j & 1));
-        T e[8];
-        memcpy(e, &v, 16);
+    for (int j = 0; j < 4; ++j) {
+      T e[8];
+      memcpy(e, &qv[nt][j], 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[j * 8 + i] = as_float(e[i]);
-          const float b = fabsf(x[j * 8 + i]);
-          if (b < INFINITY) amax = fmaxf(amax, b);
-        }
+      for (int i = 0; i < 8; ++i) {
+        x[j * 8 + i] = as_float(e[i]);
+        const float b = fabsf(x[j * 8 + i]);
+        if (b < INFINITY) amax = fmaxf(amax, b);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = 0.f;
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -416,25 +388,38 @@ __global__ void __launch_bounds__(W * 32)
       const int v = t < 2 ? (t == 0 ? valid.x : valid.y) : (t == 2 ? valid.z : valid.w);
       const int seen = all_see - base - t * kBlock;  // of unit t, by every query
       auto bytes = [](int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u; };
+      uint32_t keep[4], some[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        keep[j] = bytes(v - 4 * j);
+        some[j] = keep[j] & ~bytes(seen - 4 * j);
+      }
+      const bool tail = (some[0] | some[1] | some[2] | some[3]) != 0;
+      if (v < kBlock || tail) {
 #pragma unroll 1
-      for (int i = 0; i < 16; ++i) {  // dims 16 (i / 2) + 8 (i % 2) + g
-        uint4* at = reinterpret_cast<uint4*>(ring + value_lane + i * 8 * kBlock);
-        uint4 w = *at;
-        uint32_t bad = 0;
-        auto clear = [&](uint32_t& x, int j) {  // tokens 4 j .. + 3 of unit t
-          const uint32_t keep = bytes(v - 4 * j), some = keep & ~bytes(seen - 4 * j);
-          uint32_t b = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu) & some;
-          x &= keep & ~b;
-          for (; b; b &= ~(0xffu << ((__ffs(b) - 1) & ~7)))
-            bad |= 1u << (4 * j + ((__ffs(b) - 1) >> 3) - seen);
-        };
-        clear(w.x, 0);
-        clear(w.y, 1);
-        clear(w.z, 2);
-        clear(w.w, 3);
-        *at = w;
-        if (i & 1) nan_hi |= bad << (3 * (i >> 1));
-        else nan_lo |= bad << (3 * (i >> 1));
+        for (int i0 = 0; i0 < 16; i0 += 4) {  // dims 8 i + g, four at a time
+          uint4* at = reinterpret_cast<uint4*>(ring + value_lane + i0 * 8 * kBlock);
+          uint32_t w[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(w[i]) = at[i * 8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (tail) {
+                uint32_t b = __vcmpeq4(w[i][j] & 0x7f7f7f7fu, 0x7f7f7f7fu) & some[j];
+                w[i][j] &= ~b;
+                for (; b; b &= b - 1) bad |= 1u << (4 * j + ((__ffs(b) - 1) >> 3) - seen);
+              }
+              w[i][j] &= keep[j];
+            }
+            at[i * 8] = *reinterpret_cast<const uint4*>(w[i]);
+            const int mt = (i0 + i) >> 1;
+            if (i & 1) nan_hi |= bad << (3 * mt);
+            else nan_lo |= bad << (3 * mt);
+          }
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
@@ -525,19 +510,9 @@ __global__ void __launch_bounds__(W * 32)
     }
   }
   __syncthreads();
-  if (a.splits) asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's results
-  auto put = [&](int c, float4 acc, float m, float sum, float msum) {
-    const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
-    const float4 v = output(a, acc, m, sum, msum,
-                            (static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0 + c, lane);
-    const int64_t at = ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim + lane * 4;
-    if (a.out_fp32) store4(static_cast<float*>(a.out) + at, v);
-    else store4(static_cast<T*>(a.out) + at, v);
-  };
-  // A warp per column, four dims a lane.
-  for (int c = warp; c < cols; c += W) {
-    float mx = -INFINITY, msum = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // A column's parts, four dims a lane: of this CTA's warps, then of the
+  // cluster's CTAs, whose warps share the columns out.
+  auto of_warps = [&](int c, float4& acc, float& mx, float& msum, float& sum) {
 #pragma unroll
     for (int w = 0; w < W; ++w) mx = fmaxf(mx, pm[w * kCols + c]);
 #pragma unroll
@@ -546,9 +521,12 @@ __global__ void __launch_bounds__(W * 32)
            *reinterpret_cast<const float4*>(part + (w * kCols + c) * kHeadDim + lane * 4));
       join_sum(msum, sum, pml[w * kCols + c], pl[w * kCols + c]);
     }
-    if (cluster == 1) {
-      put(c, acc, mx, sum, msum);
-    } else {
+  };
+  if (cluster > 1) {
+    for (int c = warp; c < cols; c += W) {
+      float mx = -INFINITY, msum = -INFINITY, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      of_warps(c, acc, mx, msum, sum);
       *reinterpret_cast<float4*>(merged + c * kHeadDim + lane * 4) = acc;
       if (lane == 0) {
         mm[c] = mx;
@@ -556,19 +534,95 @@ __global__ void __launch_bounds__(W * 32)
         ml[c] = sum;
       }
     }
+    cluster_sync();
+  }
+  constexpr int kMine = (kCols + W - 1) / W;  // columns of a warp at most
+  float4 acc[kMine];
+  float sum[kMine], msum[kMine];
+  auto column = [&](int j) { return (j * cluster + rank) * W + warp; };
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int c = column(j);
+    acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum[j] = 0.f;
+    msum[j] = -INFINITY;
+    if (c >= cols) continue;
+    float mx = -INFINITY;
+    if (cluster == 1) {
+      of_warps(c, acc[j], mx, msum[j], sum[j]);
+    } else {
+      for (int i = 0; i < cluster; ++i) mx = fmaxf(mx, load_remote(mm + c, i));
+      for (int i = 0; i < cluster; ++i) {
+        add4(acc[j], scale_of(load_remote(mm + c, i), mx), load_remote4(merged + c * kHeadDim + lane * 4, i));
+        join_sum(msum[j], sum[j], load_remote(mml + c, i), load_remote(ml + c, i));
+      }
+    }
+    // From units of 2^(M - 14) to the sum's.
+    if (mx > -INFINITY) scale4(acc[j], ex2(mx - kWeightLog2 - msum[j]));
+  }
+  if (a.splits) {
+    // Join the prefix's shares: each lane a share's maximum and sum, then
+    // the shares' rows, all of the warp's columns at once.  (Plain loads: the
+    // launch that writes them may have run beside this one's beginning.)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * a.S * a.G;
+    const int64_t row0 = (static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0;
+    for (int i0 = 0; i0 < a.splits; i0 += 32) {
+      const int some = min(a.splits - i0, 32);
+      float2 st[kMine];
+      float w[kMine];
+#pragma unroll
+      for (int j = 0; j < kMine; ++j)
+        st[j] = lane < some && column(j) < cols ? __ldcg(a.stat + (i0 + lane) * rows + row0 + column(j))
+                                                : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        float top = st[j].x;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = fmaxf(top, msum[j]);
+        const float old = scale_of(msum[j], top);
+        scale4(acc[j], old);
+        w[j] = scale_of(st[j].x, top);
+        float l = w[j] * st[j].y;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        sum[j] = fmaf(sum[j], old, l);
+        msum[j] = top;
+      }
+      const float4* rest = reinterpret_cast<const float4*>(a.part) + (i0 * rows + row0) * 32 + lane;
+      constexpr int kBatch = kMine > 2 ? 4 : 8;  // rows of a column in flight
+      for (int i = 0; i < some; i += kBatch) {
+        float4 x[kMine][kBatch];
+#pragma unroll
+        for (int j = 0; j < kMine; ++j)
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+            if (column(j) < cols) x[j][b] = __ldcg(rest + (min(i + b, some - 1) * rows + column(j)) * 32);
+#pragma unroll
+        for (int j = 0; j < kMine; ++j)
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const float f = __shfl_sync(0xffffffffu, w[j], (i + b) & 31);
+            if (column(j) < cols && i + b < some) add4(acc[j], f, x[j][b]);
+          }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int c = column(j);
+    if (c >= cols) continue;
+    const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
+    const int64_t at = ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim + lane * 4;
+    // What a query sees nothing of is 0.
+    const float4 v = sum[j] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                   : make_float4(acc[j].x / sum[j], acc[j].y / sum[j], acc[j].z / sum[j],
+                                                 acc[j].w / sum[j]);
+    if (a.out_fp32) store4(static_cast<float*>(a.out) + at, v);
+    else store4(static_cast<T*>(a.out) + at, v);
   }
   if (cluster == 1) return;
-  cluster_sync();
-  for (int c = rank * W + warp; c < cols; c += cluster * W) {
-    float mx = -INFINITY, msum = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < cluster; ++i) mx = fmaxf(mx, load_remote(mm + c, i));
-    for (int i = 0; i < cluster; ++i) {
-      add4(acc, scale_of(load_remote(mm + c, i), mx), load_remote4(merged + c * kHeadDim + lane * 4, i));
-      join_sum(msum, sum, load_remote(mml + c, i), load_remote(ml + c, i));
-    }
-    put(c, acc, mx, sum, msum);
-  }
   cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
 constexpr int kAttnWarps = 4;

@@ -28,7 +28,11 @@ namespace oasis {
 namespace {
 
 constexpr int kSeg = 1024;            // entries of a segment (32 lanes x 8 x 4)
-constexpr int kVerifyWarps = 16;
+#ifndef VW
+#define VW 16
+#define VS 2
+#endif
+constexpr int kVerifyWarps = VW;
 constexpr int kMaxSegs = 1024;        // vocabularies up to 2^20
 
 // ---- four consecutive entries as floats, whatever the alignment
@@ -161,14 +165,15 @@ __global__ void __launch_bounds__(kVerifyWarps * 32)
     double* mine = sums[pass];
     for (int seg = rank * kVerifyWarps + warp; seg < segs; seg += stride) {
       Pair s[4] = {};
+      float4 x[8], y[8];  // all of the segment's loads in flight
+#pragma unroll
+      for (int i = 0; i < 8; ++i) rows.load(seg * kSeg + i * 128 + lane * 4, x[i], y[i]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float4 x, y;
-        rows.load(seg * kSeg + i * 128 + lane * 4, x, y);
-        add_rest(s[0], x.x, y.x);
-        add_rest(s[1], x.y, y.y);
-        add_rest(s[2], x.z, y.z);
-        add_rest(s[3], x.w, y.w);
+        add_rest(s[0], x[i].x, y[i].x);
+        add_rest(s[1], x[i].y, y[i].y);
+        add_rest(s[2], x[i].z, y[i].z);
+        add_rest(s[3], x[i].w, y[i].w);
       }
       Pair t = join(join(s[0], s[1]), join(s[2], s[3]));
 #pragma unroll
@@ -283,7 +288,7 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
                                  a.draft_stride % 4 == 0));
   const int segs = (a.V + kSeg - 1) / kSeg;
   int cluster = 1;
-  while (cluster < 8 && cluster * kVerifyWarps < segs && 2 * cluster * a.R <= 2 * 152) cluster *= 2;
+  while (cluster < 8 && cluster * kVerifyWarps < segs && 2 * cluster * a.R <= VS * 152) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.R) * cluster);
   cfg.blockDim = dim3(kVerifyWarps * 32);

@@ -540,21 +540,23 @@ class Oasis:
 
 
 # ------------------------------------------------- decoding over an 8-bit cache
-def _want(name: str, t: torch.Tensor, dtype, shape: tuple, device: torch.device) -> int:
-    """The address of a contiguous tensor of that type, shape and device; ValueError otherwise."""
+def _want(name: str, t: torch.Tensor, dtype, shape: tuple, device: int) -> int:
+    """The address of a contiguous tensor of that type, shape and CUDA device; ValueError
+    otherwise.  (On the path of every call: a few hundred nanoseconds.)"""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, got {t.dtype} "
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{device}, got {t.dtype} "
                          f"{list(t.shape)} on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _stream_on(s, device: torch.device) -> int:
+def _stream_on(s, device: int) -> int:
+    """The handle of stream `s`, or of the device's current stream."""
     if s is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device)
     return s if isinstance(s, int) else s.cuda_stream
 
 
@@ -592,7 +594,7 @@ class Q8Cache:
         shape = (cfg.num_pages, cfg.num_kv_heads, Q8_UNIT_BYTES)
         if pages is None:
             pages = torch.zeros(shape, dtype=torch.uint8, device=self.device)
-        _want("pages", pages, torch.uint8, shape, self.device)
+        _want("pages", pages, torch.uint8, shape, cfg.device)
         self.pages = pages
         self.workspace = torch.empty(self.sizes.workspace_bytes, dtype=torch.uint8,
                                      device=self.device)
@@ -602,6 +604,10 @@ class Q8Cache:
         if rc != OASIS_OK:
             raise OasisError(rc, "oasis_q8_init failed (misaligned pages, or CUDA error)")
         self.q8 = handle.value
+        # what every call asks of its tensors, in plain Python values
+        self._lib, self._dev = lib(), int(cfg.device)
+        self._Hq, self._Hkv, self._max_blocks = int(cfg.num_q_heads), int(cfg.num_kv_heads), int(cfg.max_blocks)
+        self._out_fp32 = bool(cfg.out_fp32)
 
     def _check(self, rc: int) -> None:
         if rc != OASIS_OK:
@@ -628,53 +634,57 @@ class Q8Cache:
 
     def _rows(self, name: str, x: torch.Tensor, T: int, dtype) -> int:
         """Elements between consecutive tokens of x [T][Hkv][d], whose heads are contiguous."""
-        H, d = self.cfg.num_kv_heads, self.cfg.head_dim
-        if x.dtype != dtype or tuple(x.shape) != (T, H, d) or x.device != self.device:
-            raise ValueError(f"{name} must be {dtype} {[T, H, d]} on {self.device}, got {x.dtype} "
+        H = self._Hkv
+        if x.dtype is not dtype or x.shape != (T, H, 128) or x.get_device() != self._dev:
+            raise ValueError(f"{name} must be {dtype} {[T, H, 128]} on {self.device}, got {x.dtype} "
                              f"{list(x.shape)} on {x.device}")
-        if T and (x.stride(2) != 1 or (H > 1 and x.stride(1) != d)):
+        st = x.stride()
+        if T and (st[2] != 1 or (H > 1 and st[1] != 128)):
             raise ValueError(f"{name}: a token's heads must be contiguous")
-        return x.stride(0) if T > 1 else 0
+        return st[0] if T > 1 else 0
 
     def oasis_q8_write(self, k, v, slots, stream=None) -> None:
         """k, v [T][Hkv][128] bf16, fp16 or fp32 (tokens may be strided), slots [T] int64."""
         T = slots.numel()
-        if k.dtype not in _TYPES:
+        typ = _TYPES.get(k.dtype)
+        if typ is None:
             raise ValueError(f"k must be bfloat16, float16 or float32, got {k.dtype}")
         ks, vs = self._rows("k", k, T, k.dtype), self._rows("v", v, T, k.dtype)
-        self._check(lib().oasis_q8_write(self.q8, k.data_ptr(), v.data_ptr(), _TYPES[k.dtype], ks, vs,
-                                         _want("slots", slots, torch.int64, (T,), self.device), T,
-                                         _stream_on(stream, self.device)))
+        self._check(self._lib.oasis_q8_write(
+            self.q8, k.data_ptr(), v.data_ptr(), typ, ks, vs,
+            _want("slots", slots, torch.int64, (T,), self._dev), T, _stream_on(stream, self._dev)))
 
     def _table(self, page_table, seq_len) -> tuple:
         R = seq_len.numel()
-        return (R, _want("page_table", page_table, torch.int32, (R, self.cfg.max_blocks), self.device),
-                _want("seq_len", seq_len, torch.int32, (R,), self.device))
+        return (R, _want("page_table", page_table, torch.int32, (R, self._max_blocks), self._dev),
+                _want("seq_len", seq_len, torch.int32, (R,), self._dev))
 
     def oasis_q8_read(self, page_table, seq_len, out, stream=None) -> None:
         """out [R][Hkv][out_blocks][2][16][128] bf16, fp16 or fp32."""
         R, table, lens = self._table(page_table, seq_len)
-        if out.dtype not in _TYPES:
+        typ = _TYPES.get(out.dtype)
+        if typ is None:
             raise ValueError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
-        blocks = int(out.shape[2]) if out.dim() == 6 else -1
-        o = _want("out", out, out.dtype, (R, self.cfg.num_kv_heads, blocks, 2, 16, 128), self.device)
-        self._check(lib().oasis_q8_read(self.q8, R, table, lens, o, _TYPES[out.dtype], blocks,
-                                        _stream_on(stream, self.device)))
+        blocks = out.shape[2] if out.dim() == 6 else -1
+        o = _want("out", out, out.dtype, (R, self._Hkv, blocks, 2, 16, 128), self._dev)
+        self._check(self._lib.oasis_q8_read(self.q8, R, table, lens, o, typ, blocks,
+                                            _stream_on(stream, self._dev)))
 
     def _queries(self, q, out, R: int) -> tuple:
-        if q.dtype not in (torch.bfloat16, torch.float16):
-            raise ValueError(f"q must be bfloat16 or float16, got {q.dtype}")
-        S = int(q.shape[0]) if q.dim() == 4 else -1
-        shape = (S, R, self.cfg.num_q_heads, self.cfg.head_dim)
-        return (S, _want("q", q, q.dtype, shape, self.device), _TYPES[q.dtype],
-                _want("out", out, torch.float32 if self.cfg.out_fp32 else q.dtype, shape, self.device))
+        dt = q.dtype
+        if dt is not torch.bfloat16 and dt is not torch.float16:
+            raise ValueError(f"q must be bfloat16 or float16, got {dt}")
+        S = q.shape[0] if q.dim() == 4 else -1
+        shape = (S, R, self._Hq, 128)
+        return (S, _want("q", q, dt, shape, self._dev), _TYPES[dt],
+                _want("out", out, torch.float32 if self._out_fp32 else dt, shape, self._dev))
 
     def oasis_q8_attn(self, q, page_table, seq_len, out, causal=False, stream=None) -> None:
         """q, out [S][R][Hq][128]."""
         R, table, lens = self._table(page_table, seq_len)
         S, qp, typ, o = self._queries(q, out, R)
-        self._check(lib().oasis_q8_attn(self.q8, R, S, 1 if causal else 0, qp, typ, table, lens, o,
-                                        _stream_on(stream, self.device)))
+        self._check(self._lib.oasis_q8_attn(self.q8, R, S, 1 if causal else 0, qp, typ, table, lens, o,
+                                            _stream_on(stream, self._dev)))
 
     def oasis_prefix_workspace(self, R: int, S: int, prefix_len: int) -> int:
         n = c_size_t(0)
@@ -694,14 +704,13 @@ class Q8Cache:
         prefix_workspace."""
         R, table, lens = self._table(page_table, seq_len)
         S, qp, typ, o = self._queries(q, out, R)
-        blocks = int(prefix_kv.shape[1]) if prefix_kv.dim() == 5 else -1
-        kv = _want("prefix_kv", prefix_kv, torch.bfloat16,
-                   (self.cfg.num_kv_heads, blocks, 2, 16, 128), self.device)
+        blocks = prefix_kv.shape[1] if prefix_kv.dim() == 5 else -1
+        kv = _want("prefix_kv", prefix_kv, torch.bfloat16, (self._Hkv, blocks, 2, 16, 128), self._dev)
         n = workspace.numel()
-        ws = _want("workspace", workspace, torch.uint8, (n,), self.device)
-        self._check(lib().oasis_prefix_attn(self.q8, R, S, 1 if causal else 0, qp, typ, kv, blocks,
-                                            prefix_len, table, lens, o, ws, n,
-                                            _stream_on(stream, self.device)))
+        ws = _want("workspace", workspace, torch.uint8, (n,), self._dev)
+        self._check(self._lib.oasis_prefix_attn(self.q8, R, S, 1 if causal else 0, qp, typ, kv, blocks,
+                                                prefix_len, table, lens, o, ws, n,
+                                                _stream_on(stream, self._dev)))
 
 
 def oasis_verify_drafts(target, draft, tokens, u_accept, u_sample, out_tokens, n_accept,
@@ -710,23 +719,26 @@ def oasis_verify_drafts(target, draft, tokens, u_accept, u_sample, out_tokens, n
     fp16 or fp32 (rows may be padded: a common stride between them), tokens [R][n] int32,
     u_accept [R][n] and u_sample [R] fp32; out_tokens [R][n + 1] and n_accept [R] int32 are
     written.  n_drafts [R] int32: drafts of each request, n where None."""
-    if target.dim() != 3 or target.dtype not in _TYPES or not target.is_cuda or target.shape[1] < 1:
+    typ = _TYPES.get(target.dtype)
+    if target.dim() != 3 or typ is None or not target.is_cuda or target.shape[1] < 1:
         raise ValueError("target must be a bfloat16, float16 or float32 CUDA tensor [R][n + 1][V]")
-    R, n, V = int(target.shape[0]), int(target.shape[1]) - 1, int(target.shape[2])
-    dev = target.device
+    R, n, V = target.shape
+    n -= 1
+    dev = target.get_device()
 
     def rows(name, x, m):
-        if x.dtype != target.dtype or tuple(x.shape) != (R, m, V) or x.device != dev:
-            raise ValueError(f"{name} must be {target.dtype} {[R, m, V]} on {dev}, got {x.dtype} "
+        if x.dtype is not target.dtype or x.shape != (R, m, V) or x.get_device() != dev:
+            raise ValueError(f"{name} must be {target.dtype} {[R, m, V]} on cuda:{dev}, got {x.dtype} "
                              f"{list(x.shape)} on {x.device}")
-        stride = x.stride(1) if m > 1 else x.stride(0) if R > 1 else V
-        if V > 1 and x.numel() and x.stride(2) != 1 or (R > 1 and m > 1 and x.stride(0) != m * stride):
+        st = x.stride()
+        stride = st[1] if m > 1 else st[0] if R > 1 else V
+        if V > 1 and R and st[2] != 1 or (R > 1 and m > 1 and st[0] != m * stride):
             raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
         return x.data_ptr(), stride
 
     p, ps = rows("target", target, n + 1)
     q, qs = rows("draft", draft, n) if draft is not None and n > 0 else (None, 0)
-    a = oasis_verify_args(R, n, V, _TYPES[target.dtype], dev.index, p, q, ps, qs,
+    a = oasis_verify_args(R, n, V, typ, dev, p, q, ps, qs,
                           _want("tokens", tokens, torch.int32, (R, n), dev),
                           None if n_drafts is None else _want("n_drafts", n_drafts, torch.int32, (R,), dev),
                           _want("u_accept", u_accept, torch.float32, (R, n), dev),
