@@ -6,23 +6,37 @@
 namespace oasis {
 namespace {
 
-// Four consecutive elements as floats.
+// Four consecutive elements, as they lie and as floats.  (The loads are
+// volatile so that a row of them is issued before the first is used.)
 template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
+struct Raw {
+  uint2 w;
+};
 template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
+struct Raw<float> {
+  uint4 w;
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load4(const T* p) {
+  Raw<T> r;
+  if constexpr (sizeof(T) == 4)
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.w.x), "=r"(r.w.y), "=r"(r.w.z), "=r"(r.w.w)
+                 : "l"(p));
+  else
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.w.x), "=r"(r.w.y) : "l"(p));
+  return r;
 }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+__device__ __forceinline__ float4 floats(const Raw<float>& r) {
+  return make_float4(__uint_as_float(r.w.x), __uint_as_float(r.w.y), __uint_as_float(r.w.z),
+                     __uint_as_float(r.w.w));
 }
-template <>
-__device__ __forceinline__ float4 load4<__half>(const __half* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+__device__ __forceinline__ float4 floats(const Raw<__nv_bfloat16>& r) {
+  return make_float4(bf16lo(r.w.x), bf16hi(r.w.x), bf16lo(r.w.y), bf16hi(r.w.y));
+}
+__device__ __forceinline__ float4 floats(const Raw<__half>& r) {
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&r.w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&r.w.y));
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
@@ -104,13 +118,13 @@ __global__ void __launch_bounds__(256) write_kernel(const Q8WriteArgs a) {
     uint32_t codes[kBlock];
     int mine = 0;  // exponent of token `lane` of the run
     if (n == kBlock) {
-      float4 v[kBlock];
+      Raw<T> v[kBlock];
 #pragma unroll
       for (int i = 0; i < kBlock; ++i) v[i] = load4(x + i * stride);
 #pragma unroll
       for (int i = 0; i < kBlock; ++i) {
         int e;
-        codes[i] = quantise_row(v[i], e);
+        codes[i] = quantise_row(floats(v[i]), e);
         if (lane == i) mine = e;
       }
       if (values) {
@@ -136,7 +150,7 @@ __global__ void __launch_bounds__(256) write_kernel(const Q8WriteArgs a) {
     } else {
       for (int i = 0; i < n; ++i) {
         int e;
-        const uint32_t c = quantise_row(load4(x + i * stride), e);
+        const uint32_t c = quantise_row(floats(load4(x + i * stride)), e);
         if (lane == i) mine = e;
         if (values) {
 #pragma unroll

@@ -10,15 +10,15 @@
 // place of 32 bits can name another token (a vocabulary's neighbouring
 // borders are about 1e-5 apart).  The sums are therefore held to about 48
 // bits: pairs of floats (an error-free sum and its remainder, as Dekker and
-// Knuth give them) inside a segment of 1024 entries, 64 bits between the
-// segments.  64-bit arithmetic throughout would bound the kernel: the card's
+// Knuth give them), two entries an instruction, and 64 bits between segments
+// of the row.  64-bit arithmetic throughout would bound the kernel: the card's
 // rate for it is two lanes a clock and SM.
 //
 // One cluster of CTAs per request reads the one or two rows that are needed
 // once, segment by segment; the segments' sums go to every CTA through
 // distributed shared memory, each finds the segment that the threshold falls
-// in, and the CTA that read it reads those 1024 entries again.  No scratch in
-// global memory, no atomics on results, one launch.
+// in, and the CTA that read it reads those entries again, all its threads
+// together.  No scratch in global memory, one launch.
 #include "common.cuh"
 #include "q8.h"
 
@@ -27,13 +27,10 @@
 namespace oasis {
 namespace {
 
-constexpr int kSeg = 1024;            // entries of a segment (32 lanes x 8 x 4)
-#ifndef VW
-#define VW 16
-#define VS 2
-#endif
-constexpr int kVerifyWarps = VW;
-constexpr int kMaxSegs = 1024;        // vocabularies up to 2^20
+constexpr int kVerifyWarps = 16;
+constexpr int kThreads = kVerifyWarps * 32;
+constexpr int kMaxSegs = 1024;        // of 1024 entries: vocabularies up to 2^20
+constexpr int kShortSeg = 256, kLongSeg = 1024;
 
 // ---- four consecutive entries as floats, whatever the alignment
 template <typename T, bool kVec>
@@ -66,30 +63,57 @@ __device__ __forceinline__ float4 row4(const T* p, int at, int V) {
 struct Pair {
   float hi, lo;
 };
-__device__ __forceinline__ void add(Pair& s, float x, float x_lo) {
-  const float t = __fadd_rn(s.hi, x);
+__device__ __forceinline__ Pair join(Pair s, Pair x) {
+  const float t = __fadd_rn(s.hi, x.hi);
   const float z = __fsub_rn(t, s.hi);
-  const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, z)), __fsub_rn(x, z));
-  s.hi = t;
-  s.lo = __fadd_rn(s.lo, __fadd_rn(e, x_lo));
-}
-// max(p - q, 0) as a pair, exactly; NaN counts as 0.
-__device__ __forceinline__ void add_rest(Pair& s, float p, float q) {
-  const float d = __fsub_rn(p, q);
-  const float b = __fsub_rn(d, p);
-  const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(q, b));
-  if (d > 0.f) add(s, d, e);
-}
-__device__ __forceinline__ Pair join(Pair a, Pair b) {
-  add(a, b.hi, b.lo);
-  return a;
+  const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, z)), __fsub_rn(x.hi, z));
+  return {t, __fadd_rn(s.lo, __fadd_rn(e, x.lo))};
 }
 __device__ __forceinline__ double value(Pair a) {
   return static_cast<double>(a.hi) + static_cast<double>(a.lo);
 }
-__device__ __forceinline__ double rest(float p, float q) {
-  const double d = static_cast<double>(p) - static_cast<double>(q);
-  return d > 0.0 ? d : 0.0;
+// max(p - q, 0) exactly, negative numbers and NaN counting as 0: with the
+// larger of the two first, the remainder of the difference takes three steps.
+__device__ __forceinline__ Pair rest(float p, float q) {
+  q = fmaxf(q, 0.f);
+  p = fmaxf(p, q);
+  const float d = __fsub_rn(p, q);
+  return {d, -__fadd_rn(q, __fsub_rn(d, p))};
+}
+// The same for two entries at a time, added to two running sums (a - b as
+// -1 * b + a, one rounding).
+struct Pair2 {
+  uint64_t hi, lo;
+};
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b, uint64_t minus) { return ffma2(b, minus, a); }
+__device__ __forceinline__ void add_rest2(Pair2& s, float p0, float p1, float q0, float q1, uint64_t minus) {
+  q0 = fmaxf(q0, 0.f);
+  q1 = fmaxf(q1, 0.f);
+  const uint64_t q = f2pack(q0, q1), p = f2pack(fmaxf(p0, q0), fmaxf(p1, q1));
+  const uint64_t d = sub2(p, q, minus);
+  const uint64_t less = fadd2(q, sub2(d, p, minus));  // minus the remainder
+  const uint64_t t = fadd2(s.hi, d), z = sub2(t, s.hi, minus);
+  const uint64_t e = fadd2(sub2(s.hi, sub2(t, z, minus), minus), sub2(d, z, minus));
+  s.hi = t;
+  s.lo = fadd2(s.lo, sub2(e, less, minus));
+}
+__device__ __forceinline__ Pair half_of(const Pair2& s, int i) {
+  float h0, h1, l0, l1;
+  f2unpack(s.hi, h0, h1);
+  f2unpack(s.lo, l0, l1);
+  return i ? Pair{h1, l1} : Pair{h0, l0};
+}
+__device__ __forceinline__ Pair shuffled(Pair a, int off) {
+  return {__shfl_xor_sync(0xffffffffu, a.hi, off), __shfl_xor_sync(0xffffffffu, a.lo, off)};
+}
+// Sums over the lanes up to this one.
+__device__ __forceinline__ Pair scan(Pair a, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const Pair o = {__shfl_up_sync(0xffffffffu, a.hi, off), __shfl_up_sync(0xffffffffu, a.lo, off)};
+    if (lane >= off) a = join(o, a);
+  }
+  return a;
 }
 
 // What a request's threshold falls on.
@@ -111,13 +135,14 @@ struct Rows {
   }
 };
 
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kVerifyWarps * 32)
-    verify_kernel(const VerifyArgs a, int cluster) {
+template <typename T, bool kVec, int kSeg>
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int cluster) {
   __shared__ double sums[2][kMaxSegs];
-  __shared__ int first_s, bad_s;
+  __shared__ int first_s, bad_s, seg_s, last_s;
+  __shared__ Pair target_s;            // the threshold, from its segment's start
+  __shared__ Pair warp_sum[kVerifyWarps];
   const int r = blockIdx.x / cluster;
-  const uint32_t rank = cluster_rank();
+  const int rank = static_cast<int>(cluster_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = a.n_drafts ? min(max(a.n_drafts[r], 0), a.n) : a.n;
   const int V = a.V;
@@ -133,22 +158,22 @@ __global__ void __launch_bounds__(kVerifyWarps * 32)
     bad_s = 0;
   }
   __syncthreads();
-  for (int i = tid; i < n; i += blockDim.x) {
+  for (int i = tid; i < n; i += kThreads) {
     const int x = tokens[i];
+    const float u = a.u_accept[static_cast<int64_t>(r) * a.n + i];
     if (x < 0 || x >= V) {
       bad_s = 1;
     } else {
       const float p = to_f(target[i * a.target_stride + x]);
       const float q = draft ? to_f(draft[i * a.draft_stride + x]) : 1.f;
-      const double u = a.u_accept[static_cast<int64_t>(r) * a.n + i];
-      if (!(u * static_cast<double>(q) < static_cast<double>(p))) atomicMin(&first_s, i);
+      if (!(static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(p))) atomicMin(&first_s, i);
     }
   }
   cluster_sync();  // also: every CTA runs before the first remote store
   const int k = first_s;
   const bool bad = bad_s != 0;
   if (rank == 0) {
-    for (int i = tid; i <= a.n; i += blockDim.x)
+    for (int i = tid; i <= a.n; i += kThreads)
       if (i != k || bad) out[i] = (i < k && !bad) ? tokens[i] : -1;
     if (tid == 0) a.n_accept[r] = bad ? -1 : k;
   }
@@ -161,121 +186,130 @@ __global__ void __launch_bounds__(kVerifyWarps * 32)
   rows.V = V;
   const int segs = (V + kSeg - 1) / kSeg;
   const int stride = cluster * kVerifyWarps;
+  const uint64_t minus = f2pack(-1.f, -1.f);
   for (int pass = 0; pass < 2; ++pass) {
     double* mine = sums[pass];
     for (int seg = rank * kVerifyWarps + warp; seg < segs; seg += stride) {
-      Pair s[4] = {};
-      float4 x[8], y[8];  // all of the segment's loads in flight
+      Pair2 s0{}, s1{};
+      constexpr int kLoads = kSeg / 128, kBatch = kLoads < 4 ? kLoads : 4;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rows.load(seg * kSeg + i * 128 + lane * 4, x[i], y[i]);
+      for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
+        float4 x[kBatch], y[kBatch];  // in flight together
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        add_rest(s[0], x[i].x, y[i].x);
-        add_rest(s[1], x[i].y, y[i].y);
-        add_rest(s[2], x[i].z, y[i].z);
-        add_rest(s[3], x[i].w, y[i].w);
+        for (int i = 0; i < kBatch; ++i) rows.load(seg * kSeg + (i0 + i) * 128 + lane * 4, x[i], y[i]);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          add_rest2(s0, x[i].x, x[i].y, y[i].x, y[i].y, minus);
+          add_rest2(s1, x[i].z, x[i].w, y[i].z, y[i].w, minus);
+        }
       }
-      Pair t = join(join(s[0], s[1]), join(s[2], s[3]));
+      Pair t = join(join(half_of(s0, 0), half_of(s0, 1)), join(half_of(s1, 0), half_of(s1, 1)));
 #pragma unroll
-      for (int off = 16; off; off >>= 1) {
-        Pair o;
-        o.hi = __shfl_xor_sync(0xffffffffu, t.hi, off);
-        o.lo = __shfl_xor_sync(0xffffffffu, t.lo, off);
-        t = join(t, o);
-      }
-      const double v = __shfl_sync(0xffffffffu, value(t), 0);
-      if (lane < cluster) store_remote(&mine[seg], lane, v);
+      for (int off = 16; off; off >>= 1) t = join(t, shuffled(t, off));
+      t = {__shfl_sync(0xffffffffu, t.hi, 0), __shfl_sync(0xffffffffu, t.lo, 0)};
+      if (lane < cluster) store_remote(&mine[seg], lane, value(t));
     }
     cluster_sync();
 
-    // Every warp: the sums before each lane's share of the segments, the
-    // total, and the segment that the threshold falls in.
-    const int share = (segs + 31) / 32;
-    double own = 0.0;
-    for (int i = 0; i < share; ++i)
-      if (lane * share + i < segs) own += mine[lane * share + i];
-    double incl = own;
+    // One warp: the sums before each lane's share of the segments, the total,
+    // and the segment that the threshold falls in.  (64-bit operations of all
+    // warps would queue for the same two lanes.)
+    if (warp == 0) {
+      const int share = (segs + 31) / 32;
+      double own = 0.0;
+      for (int i = 0; i < share; ++i)
+        if (lane * share + i < segs) own += mine[lane * share + i];
+      double incl = own;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
+      for (int off = 1; off < 32; off <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const double total = __shfl_sync(0xffffffffu, incl, 31);
+      int seg = -1;
+      double rest_of = 0.0;
+      if (total > 0.0 && total < INFINITY) {
+        const double threshold = static_cast<double>(a.u_sample[r]) * total;
+        // The lane whose share holds it; past the end (u = 1, or a rounding),
+        // the last lane with anything.
+        const unsigned over = __ballot_sync(0xffffffffu, incl > threshold && own > 0.0);
+        const unsigned some = __ballot_sync(0xffffffffu, own > 0.0);
+        const int at = over ? __ffs(over) - 1 : 31 - __clz(some);
+        double before = __shfl_sync(0xffffffffu, incl - own, at);
+        for (int i = 0; i < share && at * share + i < segs; ++i) {
+          const double v = mine[at * share + i];
+          if (v > 0.0) {
+            seg = at * share + i;
+            rest_of = threshold - before;
+            if (rest_of < v) break;
+          }
+          before += v;
+        }
+      }
+      if (lane == 0) {
+        seg_s = seg;
+        target_s.hi = static_cast<float>(rest_of);
+        target_s.lo = static_cast<float>(rest_of - static_cast<double>(target_s.hi));
+        first_s = 0x7fffffff;
+        last_s = -1;
+      }
     }
-    const double total = __shfl_sync(0xffffffffu, incl, 31);
-    if (!(total > 0.0)) {
+    __syncthreads();
+    const int seg = seg_s;
+    if (seg < 0) {
       // Nothing is left of the difference: draw from p itself.
       if (pass == 0 && (rows.q || rows.certain >= 0)) {
         rows.q = nullptr;
         rows.certain = -1;
+        __syncthreads();  // seg_s is written again
         continue;
       }
       if (rank == 0 && tid == 0) out[k] = -1;  // no entry above zero
       return;
     }
-    const double threshold = static_cast<double>(a.u_sample[r]) * total;
-    // The lane whose share holds it; past the end (u = 1, or a rounding), the
-    // last lane with anything.
-    unsigned over = __ballot_sync(0xffffffffu, incl > threshold && own > 0.0);
-    const unsigned some = __ballot_sync(0xffffffffu, own > 0.0);
-    const int at = over ? __ffs(over) - 1 : 31 - __clz(some);
-    double before = __shfl_sync(0xffffffffu, incl - own, at);
-    int seg = -1, last = -1;
-    double last_before = before;
-    for (int i = 0; i < share && at * share + i < segs; ++i) {
-      const double v = mine[at * share + i];
-      if (v > 0.0) {
-        last = at * share + i;
-        last_before = before;
-        if (before + v > threshold) {
-          seg = last;
-          break;
+    if (seg % stride / kVerifyWarps != rank) return;
+
+    // The segment again, two entries a thread: the first whose running sum
+    // exceeds the threshold; past the end, the last above zero.
+    constexpr int kWarps = kSeg / 64;
+    static_assert(kWarps <= kVerifyWarps, "two entries a thread");
+    Pair w[2] = {}, before{};
+    const int e = seg * kSeg + tid * 2;
+    if (warp < kWarps) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (e + i < V && e + i != rows.certain)
+          w[i] = rest(to_f(rows.p[e + i]), rows.q ? to_f(rows.q[e + i]) : 0.f);
+      const Pair incl = scan(join(w[0], w[1]), lane);
+      before = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+      if (lane == 0) before = {0.f, 0.f};
+      if (lane == 31) warp_sum[warp] = incl;
+    }
+    __syncthreads();
+    if (warp < kWarps) {
+      const Pair sum = scan(lane < kWarps ? warp_sum[lane] : Pair{0.f, 0.f}, lane);
+      const int left = warp > 0 ? warp - 1 : 0;
+      Pair at = {__shfl_sync(0xffffffffu, sum.hi, left), __shfl_sync(0xffffffffu, sum.lo, left)};
+      if (warp == 0) at = {0.f, 0.f};
+      at = join(join(at, before), Pair{-target_s.hi, -target_s.lo});
+      int found = 0x7fffffff, last = -1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        at = join(at, w[i]);
+        if (w[i].hi > 0.f) {
+          last = e + i;
+          if (__fadd_rn(at.hi, at.lo) > 0.f && found == 0x7fffffff) found = e + i;
         }
       }
-      before += v;
+      found = __reduce_min_sync(0xffffffffu, found);
+      last = __reduce_max_sync(0xffffffffu, last);
+      if (lane == 0) {
+        if (found != 0x7fffffff) atomicMin(&first_s, found);
+        if (last >= 0) atomicMax(&last_s, last);
+      }
     }
-    if (seg < 0) seg = last;
-    before = last_before;
-    if ((seg % stride) / kVerifyWarps != static_cast<int>(rank) || seg % kVerifyWarps != warp) return;
-
-    // The segment's own warp: 32 consecutive entries a lane, then one entry a
-    // lane of the 32 that hold the threshold.
-    Pair s[4] = {};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float4 x, y;
-      rows.load(seg * kSeg + lane * 32 + i * 4, x, y);
-      add_rest(s[0], x.x, y.x);
-      add_rest(s[1], x.y, y.y);
-      add_rest(s[2], x.z, y.z);
-      add_rest(s[3], x.w, y.w);
-    }
-    own = value(join(join(s[0], s[1]), join(s[2], s[3])));
-    incl = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
-    }
-    over = __ballot_sync(0xffffffffu, before + incl > threshold && own > 0.0);
-    const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
-    const int part = over ? __ffs(over) - 1 : 31 - __clz(any);
-    before += __shfl_sync(0xffffffffu, incl - own, part);
-    const int e = seg * kSeg + part * 32 + lane;
-    float p = 0.f, q = 0.f;
-    if (e < V && e != rows.certain) {
-      p = to_f(rows.p[e]);
-      q = rows.q ? to_f(rows.q[e]) : 0.f;
-    }
-    const double d = rest(p, q);
-    incl = d;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const double o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
-    }
-    over = __ballot_sync(0xffffffffu, before + incl > threshold && d > 0.0);
-    const unsigned pos = __ballot_sync(0xffffffffu, d > 0.0);
-    const int j = over ? __ffs(over) - 1 : 31 - __clz(pos);
-    if (lane == 0) out[k] = seg * kSeg + part * 32 + j;
+    __syncthreads();
+    if (tid == 0) out[k] = first_s != 0x7fffffff ? first_s : last_s;
     return;
   }
 }
@@ -286,12 +320,17 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
                    a.target_stride % 4 == 0 &&
                    (!a.draft || (reinterpret_cast<uintptr_t>(a.draft) % (4 * sizeof(T)) == 0 &&
                                  a.draft_stride % 4 == 0));
-  const int segs = (a.V + kSeg - 1) / kSeg;
+  // CTAs a request: as many as find a segment for each warp, up to two CTAs
+  // an SM over all requests.  Short segments where even so the long ones
+  // leave warps without work (few requests: the time is one segment's).
+  const int longs = (a.V + kLongSeg - 1) / kLongSeg;
+  const bool brief = static_cast<int64_t>(a.R) * longs < 152 * kVerifyWarps && a.V <= kMaxSegs * kShortSeg;
+  const int segs = brief ? (a.V + kShortSeg - 1) / kShortSeg : longs;
   int cluster = 1;
-  while (cluster < 8 && cluster * kVerifyWarps < segs && 2 * cluster * a.R <= VS * 152) cluster *= 2;
+  while (cluster < 8 && cluster * kVerifyWarps < segs && 2 * cluster * a.R <= 2 * 152) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.R) * cluster);
-  cfg.blockDim = dim3(kVerifyWarps * 32);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -299,8 +338,21 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return vec ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true>, a, cluster)
-             : cudaLaunchKernelEx(&cfg, verify_kernel<T, false>, a, cluster);
+  if (brief)
+    return vec ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true, kShortSeg>, a, cluster)
+               : cudaLaunchKernelEx(&cfg, verify_kernel<T, false, kShortSeg>, a, cluster);
+  return vec ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true, kLongSeg>, a, cluster)
+             : cudaLaunchKernelEx(&cfg, verify_kernel<T, false, kLongSeg>, a, cluster);
+}
+
+template <typename T>
+cudaError_t preload() {
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, verify_kernel<T, true, kShortSeg>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, verify_kernel<T, false, kShortSeg>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, verify_kernel<T, true, kLongSeg>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, verify_kernel<T, false, kLongSeg>);
+  return e;
 }
 
 }  // namespace
@@ -313,18 +365,10 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
 }
 
 cudaError_t preload_verify_kernels() {
-  cudaFuncAttributes at;
-  const void* fns[] = {reinterpret_cast<const void*>(verify_kernel<float, true>),
-                       reinterpret_cast<const void*>(verify_kernel<float, false>),
-                       reinterpret_cast<const void*>(verify_kernel<__half, true>),
-                       reinterpret_cast<const void*>(verify_kernel<__half, false>),
-                       reinterpret_cast<const void*>(verify_kernel<__nv_bfloat16, true>),
-                       reinterpret_cast<const void*>(verify_kernel<__nv_bfloat16, false>)};
-  for (const void* f : fns) {
-    const cudaError_t e = cudaFuncGetAttributes(&at, f);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  cudaError_t e = preload<float>();
+  if (e == cudaSuccess) e = preload<__half>();
+  if (e == cudaSuccess) e = preload<__nv_bfloat16>();
+  return e;
 }
 
 }  // namespace oasis

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 from typing import Optional, Sequence
 
@@ -76,6 +77,9 @@ class oasis_verify_args(ctypes.Structure):
                 ("tokens", c_void_p), ("n_drafts", c_void_p), ("u_accept", c_void_p),
                 ("u_sample", c_void_p), ("out_tokens", c_void_p), ("n_accept", c_void_p)]
 
+
+_VERIFY_ARGS = struct.Struct("@5iPPqqPPPPPP")
+assert _VERIFY_ARGS.size == ctypes.sizeof(oasis_verify_args)
 
 OASIS_BF16, OASIS_FP16, OASIS_FP32 = 0, 1, 2
 _TYPES = {torch.bfloat16: OASIS_BF16, torch.float16: OASIS_FP16, torch.float32: OASIS_FP32}
@@ -150,8 +154,8 @@ EXPORTS = {
     "oasis_prefix_workspace": (c_int, [_P, c_int, c_int, c_int, POINTER(c_size_t)]),
     "oasis_prefix_attn": (c_int, [_P, c_int, c_int, c_int, _P, c_int, _P, c_int, c_int, _P, _P,
                                   _P, _P, c_size_t, _P]),
-    "oasis_verify_error": (c_char_p, [POINTER(oasis_verify_args)]),
-    "oasis_verify_drafts": (c_int, [POINTER(oasis_verify_args), _P]),
+    "oasis_verify_error": (c_char_p, [_P]),
+    "oasis_verify_drafts": (c_int, [_P, _P]),
 }
 
 PROFILE_KINDS = ["attention", "score_topk", "admit_evict", "prefetch", "demand_score",
@@ -738,14 +742,15 @@ def oasis_verify_drafts(target, draft, tokens, u_accept, u_sample, out_tokens, n
 
     p, ps = rows("target", target, n + 1)
     q, qs = rows("draft", draft, n) if draft is not None and n > 0 else (None, 0)
-    a = oasis_verify_args(R, n, V, typ, dev, p, q, ps, qs,
+    # an oasis_verify_args, packed
+    a = _VERIFY_ARGS.pack(R, n, V, typ, dev, p, q or 0, ps, qs,
                           _want("tokens", tokens, torch.int32, (R, n), dev),
-                          None if n_drafts is None else _want("n_drafts", n_drafts, torch.int32, (R,), dev),
+                          0 if n_drafts is None else _want("n_drafts", n_drafts, torch.int32, (R,), dev),
                           _want("u_accept", u_accept, torch.float32, (R, n), dev),
                           _want("u_sample", u_sample, torch.float32, (R,), dev),
                           _want("out_tokens", out_tokens, torch.int32, (R, n + 1), dev),
                           _want("n_accept", n_accept, torch.int32, (R,), dev))
-    rc = lib().oasis_verify_drafts(ctypes.byref(a), _stream_on(stream, dev))
+    rc = lib().oasis_verify_drafts(a, _stream_on(stream, dev))
     if rc != OASIS_OK:
-        m = lib().oasis_verify_error(ctypes.byref(a))
+        m = lib().oasis_verify_error(a)
         raise OasisError(rc, m.decode() if m else "oasis_verify_drafts: CUDA error")

@@ -174,8 +174,7 @@ def verify(target, draft, x, ua, us, n_drafts=None):
         w = p[r, k]
         if k < m:
             d = q[r, k] if q is not None else (np.arange(V) == x[r, k]) * max(1.0, p[r, k, x[r, k]])
-            left = np.maximum(w - d, 0.0)
-            left[np.isnan(left)] = 0.0
+            left = np.maximum(np.where(w > 0, w, 0.0) - np.where(d > 0, d, 0.0), 0.0)  # NaN counts as 0
             if left.sum() > 0:
                 w = left
         w = np.where(w > 0, w, 0.0)
