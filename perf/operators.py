@@ -366,12 +366,13 @@ def _run_prefix(s):
 
 
 def _run_verify(s):
-    p, q, x = s["p"], s["q"], s["drafts"].long()
-    R, n = x.shape
+    p, q = s["p"], s["q"]
     if own:
         from sparse_kv_block_gb300.oasis import oasis_verify_drafts
         oasis_verify_drafts(p, q, s["drafts"], s["u_accept"], s["u_sample"], s["tokens"], s["n_accept"])
         return s["tokens"], s["n_accept"]
+    x = s["drafts"].long()
+    R, n = x.shape
     px = p[:, :n].gather(2, x.unsqueeze(-1)).squeeze(-1).double()
     qx = q.gather(2, x.unsqueeze(-1)).squeeze(-1).double() if q is not None else torch.ones_like(px)
     ok = s["u_accept"].double() * qx < px
