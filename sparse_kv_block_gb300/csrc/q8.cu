@@ -72,8 +72,14 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
                : "memory");
 }
 
+constexpr int kWriteWarps = 4;
+
 // Rounding into the pages.  Bound by memory: 256 values are read and 258
-// bytes written a token and head.
+// bytes written a token and head.  What holds it back is latency (the slots,
+// then the rows): 16 rows a warp are asked for at once, and seven CTAs of
+// four warps an SM were the best of what registers allow (32768 tokens x 8
+// heads, bf16: 39.6 us = 5.1 TB/s; six 42, eight 41, nine 48, ten 50; CTAs of
+// eight warps 43 to 53).
 //
 // Values are stored with a block's tokens consecutive, so single tokens mean
 // single bytes 16 apart; whole blocks are worth finding.  The tokens are cut
@@ -83,7 +89,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
 // begins there, reading on past its span where the run does; a run that is a
 // whole block is transposed in registers and stored in whole sectors.
 template <typename T, int kSpan>
-__global__ void __launch_bounds__(256) write_kernel(const Q8WriteArgs a) {
+__global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 4 ? 5 : 7) write_kernel(const Q8WriteArgs a) {
   static_assert(kSpan <= kBlock, "a run from the span's last place ends within 32 lanes");
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -253,9 +259,9 @@ cudaError_t launch_write(const Q8WriteArgs& a, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.T) * a.Hkv * 2;
   const bool one = rows < 152 * 64;
   const int64_t items = one ? rows : (static_cast<int64_t>(a.T) + kLongSpan - 1) / kLongSpan * a.Hkv * 2;
-  const unsigned grid = static_cast<unsigned>((items + 7) / 8);
-  if (one) write_kernel<T, 1><<<grid, 256, 0, s>>>(a);
-  else write_kernel<T, kLongSpan><<<grid, 256, 0, s>>>(a);
+  const unsigned grid = static_cast<unsigned>((items + kWriteWarps - 1) / kWriteWarps);
+  if (one) write_kernel<T, 1><<<grid, kWriteWarps * 32, 0, s>>>(a);
+  else write_kernel<T, kLongSpan><<<grid, kWriteWarps * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
 
