@@ -17,9 +17,11 @@
 // maximum is only moved when a row's grows by more than 2^8, so the outputs
 // are seldom rescaled.
 //
-// Each share writes its rows' unnormalised outputs, maxima and sums; the
-// attention over the requests' own pages joins them in its last step.
-#include "common.cuh"
+// Each share writes its rows' unnormalised outputs, maxima and sums, as the
+// attention over the requests' own pages does.  Three launches that overlap:
+// this one; the pages' share, bound by latency and memory, on the SMs that
+// are idle or get free; the join, a warp a row.
+#include "q8.cuh"
 #include "q8.h"
 
 namespace oasis {
@@ -37,7 +39,8 @@ struct PrefixLayout {
   static constexpr int kQ = 0;
   static constexpr int kRing = kTiles * kStageBytes;
   static constexpr int kBars = kRing + kRingStages * kStageBytes;
-  static constexpr int kBytes = kBars + 256 + 1024;        // + alignment
+  static constexpr int kRows = kBars + 256;                // where a row's query begins
+  static constexpr int kBytes = kRows + kTiles * kTile * 4 + 1024;  // + alignment
   static constexpr int kColumns = kTiles * 256;            // tensor memory
 };
 
@@ -131,12 +134,6 @@ __device__ __forceinline__ void load_blocks(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 32 bytes, a whole sector.
 __device__ __forceinline__ void store8(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
@@ -160,7 +157,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   uint64_t* drain = o_done + 2;
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
 
-  asm volatile("griddepcontrol.launch_dependents;");  // the page attention may take idle SMs
+  asm volatile("griddepcontrol.launch_dependents;");  // the pages' share takes the SMs this leaves idle
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_tile = blockIdx.x % a.row_tiles;
   const int h = (blockIdx.x / a.row_tiles) % a.Hkv;
@@ -195,31 +192,31 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
     for (; loaded < 2 * n && loaded < kRingStages; ++loaded) load(loaded);
   }
   if (warp == kTiles * 4 + 1) tmem_alloc(tmem_s, Lay::kColumns);
-  // The query rows, half a warp a row, as the swizzle places them; a few rows
-  // at a time so that their loads are in flight together.
+  // The query rows: where each begins (one division a row), then half a warp a
+  // row, all of a thread's loads in flight, to where the swizzle has them.
+  int* begin = reinterpret_cast<int*>(smem + Lay::kRows);
+  for (int rr = threadIdx.x; rr < kTiles * kTile; rr += Lay::kThreads) {
+    const int row = row0 + rr, r = row / per_request, c = row - r * per_request, s = c / a.G;
+    begin[rr] = row < rows ? (s * a.R + r) * a.Hq + h * a.G + c - s * a.G : -1;
+  }
+  __syncthreads();
   {
-    constexpr int kBatch = 8, kStep = Lay::kThreads / 16;
-    const int ch = threadIdx.x & 15;
-    for (int r0 = threadIdx.x >> 4; r0 < kTiles * kTile; r0 += kBatch * kStep) {
-      uint4 v[kBatch];
+    constexpr int kStep = Lay::kThreads / 16, kLoads = (kTiles * kTile + kStep - 1) / kStep;
+    const int ch = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+    uint4 v[kLoads];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int rr = r0 + b * kStep, row = row0 + rr;
-        v[b] = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < kTiles * kTile && row < rows) {
-          const int r = row / per_request, c = row - r * per_request, s = c / a.G;
-          v[b] = __ldg(reinterpret_cast<const uint4*>(
-              static_cast<const __nv_bfloat16*>(a.q) +
-              ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + c - s * a.G) * kHeadDim + ch * 8));
-        }
-      }
+    for (int b = 0; b < kLoads; ++b) {
+      const int rr = r0 + b * kStep;
+      const int at = rr < kTiles * kTile ? begin[rr] : -1;
+      v[b] = make_uint4(0u, 0u, 0u, 0u);
+      if (at >= 0) v[b] = __ldg(static_cast<const uint4*>(a.q) + static_cast<int64_t>(at) * 16 + ch);
+    }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int rr = r0 + b * kStep;
-        if (rr < kTiles * kTile) {
-          uint8_t* tile = smem + Lay::kQ + (rr / kTile) * kStageBytes + (ch >> 3) * kHalfTile;
-          *reinterpret_cast<uint4*>(tile + (rr % kTile) * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[b];
-        }
+    for (int b = 0; b < kLoads; ++b) {
+      const int rr = r0 + b * kStep;
+      if (rr < kTiles * kTile) {
+        uint8_t* tile = smem + Lay::kQ + (rr / kTile) * kStageBytes + (ch >> 3) * kHalfTile;
+        *reinterpret_cast<uint4*>(tile + (rr % kTile) * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v[b];
       }
     }
   }
@@ -409,6 +406,58 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   if (warp == kTiles * 4 + 1) tmem_free(tmem, Lay::kColumns);
 }
 
+// The shares' rows joined: a warp a row, each lane a share's maximum and sum,
+// then four dims of every share.  (Plain loads: the launches that write them
+// may have run beside this one's beginning.)
+template <typename T>
+__global__ void __launch_bounds__(128) join_kernel(const PrefixArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int per_request = a.S * a.G;
+  const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * per_request;
+  if (row >= rows) return;
+  const int c = static_cast<int>(row % per_request), s = c / a.G;
+  const int64_t hr = row / per_request;
+  const int h = static_cast<int>(hr / a.R), r = static_cast<int>(hr % a.R);
+  T* out = static_cast<T*>(a.out) +
+           ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + c - s * a.G) * kHeadDim + lane * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int shares = a.splits + 1;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, sum = 0.f;
+  for (int i0 = 0; i0 < shares; i0 += 32) {
+    const int some = min(shares - i0, 32);
+    constexpr int kBatch = 8;
+    const float2 st = lane < some ? __ldcg(a.stat + (i0 + lane) * rows + row) : make_float2(-INFINITY, 0.f);
+    const float4* part = reinterpret_cast<const float4*>(a.part) + (i0 * rows + row) * 32 + lane;
+    float4 x[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) x[b] = __ldcg(part + min(b, some - 1) * rows * 32);
+    float top = st.x;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    top = fmaxf(top, m);
+    const float old = scale_of(m, top), w = scale_of(st.x, top);
+    float l = w * st.y;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    sum = fmaf(sum, old, l);
+    scale4(acc, old);
+    m = top;
+    for (int i = 0; i < some; i += kBatch) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float f = __shfl_sync(0xffffffffu, w, (i + b) & 31);
+        if (i + b < some) add4(acc, f, x[b]);
+      }
+      if (i + kBatch < some)
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) x[b] = __ldcg(part + min(i + kBatch + b, some - 1) * rows * 32);
+    }
+  }
+  store4(out, make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum));
+}
+
 }  // namespace
 
 PrefixShape prefix_shape(int R, int S, int G, int Hkv, int prefix_len) {
@@ -419,26 +468,57 @@ PrefixShape prefix_shape(int R, int S, int G, int Hkv, int prefix_len) {
   p.row_tiles = static_cast<int>((rows + p.tiles * kTile - 1) / (p.tiles * kTile));
   const int64_t units = static_cast<int64_t>(p.row_tiles) * Hkv;
   const int all = (prefix_len + kTile - 1) / kTile;
+  // As many shares as give every SM a CTA, but no more than shorten the
+  // longest: the SMs left over are the pages' share's.
   int64_t splits = units > 0 ? 152 / units : 1;
   if (splits > all) splits = all;
-  p.splits = splits < 1 ? 1 : static_cast<int>(splits);
-  const int64_t vectors = p.splits * static_cast<int64_t>(Hkv) * rows;
+  if (splits < 1) splits = 1;
+  if (all > 0) {
+    const int64_t longest = (all + splits - 1) / splits;
+    splits = (all + longest - 1) / longest;
+  }
+  p.splits = static_cast<int>(splits);
+  const int64_t vectors = (p.splits + 1) * static_cast<int64_t>(Hkv) * rows;
   p.part_bytes = static_cast<size_t>(vectors) * kHeadDim * 4;
   p.bytes = p.part_bytes + static_cast<size_t>(vectors) * 8;
   return p;
 }
 
 namespace {
-template <int kTiles>
-cudaError_t launch_tiles(const PrefixArgs& a, const CUtensorMap& map, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.row_tiles) * a.Hkv * a.splits;
-  prefix_kernel<kTiles><<<grid, PrefixLayout<kTiles>::kThreads, PrefixLayout<kTiles>::kBytes, s>>>(a, map);
-  return cudaGetLastError();
+
+// A launch that may begin while the one before it still runs.
+template <typename... Params, typename... Args>
+cudaError_t launch_beside(void (*kernel)(Params...), unsigned grid, int threads, int smem, cudaStream_t s,
+                          const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
 }  // namespace
 
 cudaError_t launch_prefix(const PrefixArgs& a, int tiles, const CUtensorMap& map, cudaStream_t s) {
-  return tiles == 2 ? launch_tiles<2>(a, map, s) : launch_tiles<1>(a, map, s);
+  const unsigned grid = static_cast<unsigned>(a.row_tiles) * a.Hkv * a.splits;
+  if (tiles == 2)
+    prefix_kernel<2><<<grid, PrefixLayout<2>::kThreads, PrefixLayout<2>::kBytes, s>>>(a, map);
+  else
+    prefix_kernel<1><<<grid, PrefixLayout<1>::kThreads, PrefixLayout<1>::kBytes, s>>>(a, map);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_join(const PrefixArgs& a, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * a.S * a.G;
+  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  return a.out_fp32 ? launch_beside(join_kernel<float>, grid, 128, 0, s, a)
+                    : launch_beside(join_kernel<__nv_bfloat16>, grid, 128, 0, s, a);
 }
 
 cudaError_t preload_prefix_kernels() {
@@ -447,6 +527,9 @@ cudaError_t preload_prefix_kernels() {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(prefix_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              PrefixLayout<2>::kBytes);
+  cudaFuncAttributes at;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, join_kernel<float>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, join_kernel<__nv_bfloat16>);
   return e;
 }
 

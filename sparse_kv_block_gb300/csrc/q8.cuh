@@ -66,4 +66,48 @@ __device__ __forceinline__ uint32_t q8_unpack2(uint32_t codes) {
   return r;
 }
 
+// 2^x, to two units in the last place (results under 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ---- parts of a softmax, each (outputs, sum) in units of 2^m
+// 2^(m - mx); where no part has seen a score (mx = -inf) the parts are zeros,
+// or NaN, and are added as they are.
+__device__ __forceinline__ float scale_of(float m, float mx) {
+  return mx == -INFINITY ? 1.f : ex2(m - mx);
+}
+__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
+// The sums (m, l) and (m2, l2), each in units of 2^m, as one.
+__device__ __forceinline__ void join_sum(float& m, float& l, float m2, float l2) {
+  const float mx = fmaxf(m, m2);
+  l = l * scale_of(m, mx) + l2 * scale_of(m2, mx);
+  m = mx;
+}
+__device__ __forceinline__ void scale4(float4& a, float f) {
+  a.x *= f;
+  a.y *= f;
+  a.z *= f;
+  a.w *= f;
+}
+__device__ __forceinline__ void add4(float4& a, float f, const float4& x) {
+  a.x = fmaf(f, x.x, a.x);
+  a.y = fmaf(f, x.y, a.y);
+  a.z = fmaf(f, x.z, a.z);
+  a.w = fmaf(f, x.w, a.w);
+}
+__device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ void store4(__half* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+}
+
 }  // namespace oasis

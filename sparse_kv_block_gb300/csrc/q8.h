@@ -45,12 +45,10 @@ struct Q8AttnArgs {
   int causal, type, out_fp32;
   float scale_log2;          // softmax scale * log2(e)
   long long wait_limit;
-  // What the launch before this one found for a prefix that all requests
-  // share (splits > 0), of row r * S * G + s * G + gi: outputs [splits][Hkv]
-  // [R * S * G][d] in units of 2^m over their sums, and (m, sum).
-  const float* part;
-  const float2* stat;
-  int splits;
+  // Set: the outputs go here instead, as one share of a softmax: row (h * R +
+  // r) * S * G + s * G + gi [d] in units of 2^m, and (m, sum).
+  float* part;
+  float2* stat;
 };
 
 // Shares and row tiles of the prefix attention, and its scratch.
@@ -58,16 +56,18 @@ struct PrefixShape {
   int64_t rows;      // R * S * G
   int tiles;         // 128-row tiles a CTA, 1 or 2
   int row_tiles;     // CTAs over the rows
-  int splits;        // shares of the prefix
+  int splits;        // shares of the prefix; one more is the requests' own pages
   size_t part_bytes, bytes;
 };
 
 struct PrefixArgs {
   const void* q;             // [S][R][Hq][d] bf16
-  float* part;               // [splits][Hkv][rows][d]
-  float2* stat;              // [splits][Hkv][rows]
+  void* out;                 // [S][R][Hq][d] bf16 or fp32
+  float* part;               // [splits + 1][Hkv][rows][d]
+  float2* stat;              // [splits + 1][Hkv][rows]
   uint32_t* err;
   int R, S, Hq, Hkv, G, prefix_len, row_tiles, splits;
+  int out_fp32;
   float scale_log2;
   long long wait_limit;
 };
@@ -91,7 +91,10 @@ cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s);
 PrefixShape prefix_shape(int R, int S, int G, int Hkv, int prefix_len);
 // The map covers the prefix [Hkv][blocks][2][B][d] with boxes of 8 blocks'
 // keys or values, 64 dims.
+// Then launch_q8_attn with `part` set (it may run beside this one), then
+// launch_join, which waits for both.
 cudaError_t launch_prefix(const PrefixArgs& a, int tiles, const CUtensorMap& map, cudaStream_t s);
+cudaError_t launch_join(const PrefixArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 
 // Load the kernels' code (and set their shared memory) on the current device.

@@ -312,33 +312,34 @@ OASIS_API int oasis_prefix_attn(oasis_q8* q8, int num_requests, int num_queries,
   if (num_requests == 0) return OASIS_OK;
   OnDevice dev(q8->cfg.device);
   if (int rc = q8->cuda(dev.error(), "cudaSetDevice")) return rc;
-  if (prefix_len > 0) {
-    const PrefixShape sh = prefix_shape(num_requests, num_queries, q8->G, q8->cfg.num_kv_heads, prefix_len);
-    CUtensorMap map;
-    if (int rc = prefix_map(q8, prefix_kv, prefix_blocks, &map)) return rc;
-    PrefixArgs p{};
-    p.q = q;
-    p.part = static_cast<float*>(workspace);
-    p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + sh.part_bytes);
-    p.err = q8->err;
-    p.R = num_requests;
-    p.S = num_queries;
-    p.Hq = q8->cfg.num_q_heads;
-    p.Hkv = q8->cfg.num_kv_heads;
-    p.G = q8->G;
-    p.prefix_len = prefix_len;
-    p.row_tiles = sh.row_tiles;
-    p.splits = sh.splits;
-    p.scale_log2 = q8->scale_log2;
-    p.wait_limit = kWaitLimitCycles;
-    if (int rc = q8->cuda(launch_prefix(p, sh.tiles, map, static_cast<cudaStream_t>(stream)),
-                          "prefix_attn launch"))
-      return rc;
-    a.part = p.part;
-    a.stat = p.stat;
-    a.splits = sh.splits;
-  }
-  return q8->cuda(launch_q8_attn(a, static_cast<cudaStream_t>(stream)), "prefix_attn launch");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (prefix_len == 0) return q8->cuda(launch_q8_attn(a, st), "prefix_attn launch");
+  const PrefixShape sh = prefix_shape(num_requests, num_queries, q8->G, q8->cfg.num_kv_heads, prefix_len);
+  CUtensorMap map;
+  if (int rc = prefix_map(q8, prefix_kv, prefix_blocks, &map)) return rc;
+  PrefixArgs p{};
+  p.q = q;
+  p.out = out;
+  p.part = static_cast<float*>(workspace);
+  p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + sh.part_bytes);
+  p.err = q8->err;
+  p.R = num_requests;
+  p.S = num_queries;
+  p.Hq = q8->cfg.num_q_heads;
+  p.Hkv = q8->cfg.num_kv_heads;
+  p.G = q8->G;
+  p.prefix_len = prefix_len;
+  p.row_tiles = sh.row_tiles;
+  p.splits = sh.splits;
+  p.out_fp32 = q8->cfg.out_fp32;
+  p.scale_log2 = q8->scale_log2;
+  p.wait_limit = kWaitLimitCycles;
+  const int64_t share = static_cast<int64_t>(sh.splits) * p.Hkv * sh.rows;  // the pages' share
+  a.part = p.part + share * kHeadDim;
+  a.stat = p.stat + share;
+  if (int rc = q8->cuda(launch_prefix(p, sh.tiles, map, st), "prefix_attn launch")) return rc;
+  if (int rc = q8->cuda(launch_q8_attn(a, st), "prefix_attn launch (pages)")) return rc;
+  return q8->cuda(launch_join(p, st), "prefix_attn launch (join)");
 }
 
 OASIS_API const char* oasis_verify_error(const oasis_verify_args* a) {

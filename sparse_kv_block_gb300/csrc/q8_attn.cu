@@ -57,12 +57,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// 2^x, to two units in the last place (results under 2^-126 are 0).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
@@ -75,43 +69,6 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) 
 }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// 2^(m - mx); where no part has seen a score (mx = -inf) the parts are zeros,
-// or NaN, and are added as they are.
-__device__ __forceinline__ float scale_of(float m, float mx) {
-  return mx == -INFINITY ? 1.f : ex2(m - mx);
-}
-__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
-// The sums (m, l) and (m2, l2), each in units of 2^m, as one.
-__device__ __forceinline__ void join_sum(float& m, float& l, float m2, float l2) {
-  const float mx = fmaxf(m, m2);
-  l = l * scale_of(m, mx) + l2 * scale_of(m2, mx);
-  m = mx;
-}
-__device__ __forceinline__ void scale4(float4& a, float f) {
-  a.x *= f;
-  a.y *= f;
-  a.z *= f;
-  a.w *= f;
-}
-__device__ __forceinline__ void add4(float4& a, float f, const float4& x) {
-  a.x = fmaf(f, x.x, a.x);
-  a.y = fmaf(f, x.y, a.y);
-  a.z = fmaf(f, x.z, a.z);
-  a.w = fmaf(f, x.w, a.w);
-}
-
-__device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
-__device__ __forceinline__ void store4(__half* p, const float4& v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
-}
 
 template <typename T, int W, int kNT>
 __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory allows
@@ -119,6 +76,7 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
   using Lay = Layout<W, kNT>;
   constexpr int kCols = Lay::kCols;
   extern __shared__ __align__(128) uint8_t smem[];
+  if (a.part) asm volatile("griddepcontrol.launch_dependents;");  // the join may begin
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int pair = blockIdx.x / cluster;
@@ -560,59 +518,16 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
     // From units of 2^(M - 14) to the sum's.
     if (mx > -INFINITY) scale4(acc[j], ex2(mx - kWeightLog2 - msum[j]));
   }
-  if (a.splits) {
-    // Join the prefix's shares: each lane a share's maximum and sum, then
-    // the shares' rows, all of the warp's columns at once.  (Plain loads: the
-    // launch that writes them may have run beside this one's beginning.)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * a.S * a.G;
-    const int64_t row0 = (static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0;
-    for (int i0 = 0; i0 < a.splits; i0 += 32) {
-      const int some = min(a.splits - i0, 32);
-      float2 st[kMine];
-      float w[kMine];
-#pragma unroll
-      for (int j = 0; j < kMine; ++j)
-        st[j] = lane < some && column(j) < cols ? __ldcg(a.stat + (i0 + lane) * rows + row0 + column(j))
-                                                : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int j = 0; j < kMine; ++j) {
-        float top = st[j].x;
-#pragma unroll
-        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        top = fmaxf(top, msum[j]);
-        const float old = scale_of(msum[j], top);
-        scale4(acc[j], old);
-        w[j] = scale_of(st[j].x, top);
-        float l = w[j] * st[j].y;
-#pragma unroll
-        for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        sum[j] = fmaf(sum[j], old, l);
-        msum[j] = top;
-      }
-      const float4* rest = reinterpret_cast<const float4*>(a.part) + (i0 * rows + row0) * 32 + lane;
-      constexpr int kBatch = kMine > 2 ? 4 : 8;  // rows of a column in flight
-      for (int i = 0; i < some; i += kBatch) {
-        float4 x[kMine][kBatch];
-#pragma unroll
-        for (int j = 0; j < kMine; ++j)
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b)
-            if (column(j) < cols) x[j][b] = __ldcg(rest + (min(i + b, some - 1) * rows + column(j)) * 32);
-#pragma unroll
-        for (int j = 0; j < kMine; ++j)
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b) {
-            const float f = __shfl_sync(0xffffffffu, w[j], (i + b) & 31);
-            if (column(j) < cols && i + b < some) add4(acc[j], f, x[j][b]);
-          }
-      }
-    }
-  }
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     const int c = column(j);
     if (c >= cols) continue;
+    if (a.part) {  // a share among others, joined later
+      const int64_t at = (static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0 + c;
+      store4(a.part + at * kHeadDim + lane * 4, acc[j]);
+      if (lane == 0) a.stat[at] = make_float2(msum[j], sum[j]);
+      continue;
+    }
     const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
     const int64_t at = ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim + lane * 4;
     // What a query sees nothing of is 0.
@@ -622,6 +537,11 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
     if (a.out_fp32) store4(static_cast<float*>(a.out) + at, v);
     else store4(static_cast<T*>(a.out) + at, v);
   }
+  // Beside another launch that writes shares: who waits for this grid has to
+  // have waited for that one.  One CTA does it for all (others would keep SMs
+  // from the CTAs behind them).
+  if (a.part && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
   if (cluster == 1) return;
   cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
@@ -658,12 +578,10 @@ cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = cluster;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  // Behind a prefix's launch: may start while that one still runs, and waits
-  // for its results before the last join.
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // beside the prefix's launch
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = a.splits ? 2 : 1;
+  cfg.numAttrs = a.part ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, attn_kernel<T, kAttnWarps, kNT>, a, cluster);
 }
 
