@@ -41,12 +41,14 @@ struct Layout {
   static constexpr int kCols = 8 * kNT;
   static constexpr int kRing = W * kGroupBytes;              // one group a warp
   static constexpr int kPartial = kCols * kHeadDim * 4;      // one warp's partial output
-  static_assert(W * kPartial <= kRing, "the warps' partial outputs reuse the ring");
+  static_assert((W + 1) * kPartial + 3 * kCols * 4 <= kRing, "the partial outputs reuse the ring");
+  static constexpr int kMerged = W * kPartial;               // the CTA's [kCols][d], then [kCols] M, L, sums
   static constexpr int kBars = kRing;                        // keys' and values' barrier a warp
   static constexpr int kValid = kBars + W * 16;              // int4 for even and odd groups
   static constexpr int kStat = kValid + W * 32;              // [W][kCols] M, L, sums
-  static constexpr int kMerged = kStat + 3 * W * kCols * 4;  // [kCols][d], then [kCols] M, L, sums
-  static constexpr int kBytes = kMerged + kPartial + 3 * kCols * 4;
+  static constexpr int kFactor = kStat + 3 * W * kCols * 4;  // of a column's scores
+  static constexpr int kQuery = kFactor + kCols * 4;         // [kNT][8][32 lanes] fragments
+  static constexpr int kBytes = kQuery + kNT * 8 * 32 * 8;
 };
 
 // 16 bytes of shared memory.  (An ordinary load: the compiler may move it,
@@ -71,7 +73,7 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 
 template <typename T, int W, int kNT>
-__global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory allows
+__global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
     attn_kernel(const Q8AttnArgs a, int cluster) {
   using Lay = Layout<W, kNT>;
   constexpr int kCols = Lay::kCols;
@@ -106,19 +108,18 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
   };
   int len = __ldg(a.len + r);
   int page = page_of(0);
-  uint4 qv[kNT][4];  // of column g of a tile: dims 64 (j / 2) + 16 t + 8 (j % 2) .. + 7
-#pragma unroll
-  for (int nt = 0; nt < kNT; ++nt) {
-    const int c = col0 + nt * 8 + g;
-    if (nt * 8 + g < cols) {
+  uint4 qv[4];  // warp nt < kNT: of column 8 nt + g, dims 64 (j / 2) + 16 t + 8 (j % 2) .. + 7
+  {
+    const int c = col0 + warp * 8 + g;
+    if (warp < kNT && warp * 8 + g < cols) {
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const T*>(a.q) +
           ((static_cast<int64_t>(c / a.G) * a.R + r) * a.Hq + h * a.G + c % a.G) * kHeadDim);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) qv[nt][j] = __ldg(src + (j >> 1) * 8 + t * 2 + (j & 1));
+      for (int j = 0; j < 4; ++j) qv[j] = __ldg(src + (j >> 1) * 8 + t * 2 + (j & 1));
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) qv[nt][j] = make_uint4(0u, 0u, 0u, 0u);
+      for (int j = 0; j < 4; ++j) qv[j] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   len = max(len, 0);
@@ -158,19 +159,19 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
     issue_values();
   }
 
-  // Query columns as B fragments.  Step (j, w) of the contraction covers, for
-  // lane t, dims 64 j + 16 t + 4 w .. + 3.
-  uint32_t qf[kNT][8][2];
-  float f0[kNT], f1[kNT];        // score factors of columns 2 t, 2 t + 1
-  int lim0[kNT], lim1[kNT];      // tokens those columns see
-#pragma unroll
-  for (int nt = 0; nt < kNT; ++nt) {
+  // Query columns as B fragments, in shared memory (registers for them would
+  // cost a third of the CTAs an SM holds): warp nt makes those of tile nt.
+  // Step (j, w) of the contraction covers, for lane t, dims 64 j + 16 t + 4 w
+  // .. + 3.
+  float* factor = reinterpret_cast<float*>(smem + Lay::kFactor);
+  uint2* query = reinterpret_cast<uint2*>(smem + Lay::kQuery);
+  if (warp < kNT) {
     float x[32];
     float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       T e[8];
-      memcpy(e, &qv[nt][j], 16);
+      memcpy(e, &qv[j], 16);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[j * 8 + i] = as_float(e[i]);
@@ -183,13 +184,18 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
     const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 13, -100);
     const float down = pow2f(-e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      qf[nt][i][0] = pack_f16x2(x[4 * i] * down, x[4 * i + 1] * down);
-      qf[nt][i][1] = pack_f16x2(x[4 * i + 2] * down, x[4 * i + 3] * down);
-    }
-    const float f = a.scale_log2 * pow2f(e);
-    f0[nt] = __shfl_sync(0xffffffffu, f, 8 * t);
-    f1[nt] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+    for (int i = 0; i < 8; ++i)
+      query[(warp * 8 + i) * 32 + lane] = make_uint2(pack_f16x2(x[4 * i] * down, x[4 * i + 1] * down),
+                                                     pack_f16x2(x[4 * i + 2] * down, x[4 * i + 3] * down));
+    if (t == 0) factor[warp * 8 + g] = a.scale_log2 * pow2f(e);
+  }
+  __syncthreads();
+  float f0[kNT], f1[kNT];        // score factors of columns 2 t, 2 t + 1
+  int lim0[kNT], lim1[kNT];      // tokens those columns see
+#pragma unroll
+  for (int nt = 0; nt < kNT; ++nt) {
+    f0[nt] = factor[nt * 8 + 2 * t];
+    f1[nt] = factor[nt * 8 + 2 * t + 1];
     const int c0 = col0 + nt * 8 + 2 * t;
     lim0[nt] = a.causal ? len - (a.S - 1 - c0 / a.G) : len;
     lim1[nt] = a.causal ? len - (a.S - 1 - (c0 + 1) / a.G) : len;
@@ -223,24 +229,34 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
     const bool whole = min(min(valid.x, valid.y), min(valid.z, valid.w)) == kBlock &&
                        base + kGroupTokens <= all_see;
 
-    // Scores: S^T (64 tokens x columns), four steps of 16 tokens.
+    // Scores: S^T (64 tokens x columns), four steps of 16 tokens.  The steps go
+    // side by side, so that neighbouring products do not wait on one another.
     float s[kNT][4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) s[nt][i][0] = s[nt][i][1] = s[nt][i][2] = s[nt][i][3] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 2; ++j) {
+      uint4 lo[4], hi[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         const uint8_t* at = sb + key_lane + ((j ^ (g & 1)) << 6) + i * 4 * kHeadDim;
-        const uint4 lo = lds128(at), hi = lds128(at + 2 * kHeadDim);
+        lo[i] = lds128(at);
+        hi[i] = lds128(at + 2 * kHeadDim);
+      }
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < 4; ++w) {
+        uint2 q[kNT];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) q[nt] = query[(nt * 8 + j * 4 + w) * 32 + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           uint32_t a0, a1, a2, a3;
-          unpack4(word(lo, w), a0, a2);
-          unpack4(word(hi, w), a1, a3);
+          unpack4(word(lo[i], w), a0, a2);
+          unpack4(word(hi[i], w), a1, a3);
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-            mma_f16_16816(s[nt][i], a0, a1, a2, a3, qf[nt][j * 4 + w][0], qf[nt][j * 4 + w][1]);
+          for (int nt = 0; nt < kNT; ++nt) mma_f16_16816(s[nt][i], a0, a1, a2, a3, q[nt].x, q[nt].y);
         }
       }
     }
@@ -389,17 +405,24 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
 
     // Outputs: O^T (128 dims x columns) += V^T P^T.
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      const uint4 lo = lds128(sb + value_lane + mt * 16 * kBlock);
-      const uint4 hi = lds128(sb + value_lane + mt * 16 * kBlock + 8 * kBlock);
+    for (int mt = 0; mt < 8; mt += 2) {
+      uint4 lo[2], hi[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        lo[b] = lds128(sb + value_lane + (mt + b) * 16 * kBlock);
+        hi[b] = lds128(sb + value_lane + (mt + b) * 16 * kBlock + 8 * kBlock);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t a0, a1, a2, a3;
-        unpack4(word(lo, i), a0, a2);
-        unpack4(word(hi, i), a1, a3);
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-          mma_f16_16816(o[nt][mt], a0, a1, a2, a3, pb[nt][i][0], pb[nt][i][1]);
+        for (int b = 0; b < 2; ++b) {
+          uint32_t a0, a1, a2, a3;
+          unpack4(word(lo[b], i), a0, a2);
+          unpack4(word(hi[b], i), a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+            mma_f16_16816(o[nt][mt + b], a0, a1, a2, a3, pb[nt][i][0], pb[nt][i][1]);
+        }
       }
     }
     if (__any_sync(0xffffffffu, (nan_lo | nan_hi) != 0)) {
@@ -545,13 +568,17 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)  // as shared memory
   if (cluster == 1) return;
   cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
-constexpr int kAttnWarps = 4;
+#ifndef W2
+#define W2 4
+#endif
+template <int kNT>
+constexpr int kAttnWarps = kNT == 1 ? 4 : W2;
 
 template <typename T, int kNT>
 cudaError_t configure() {
-  return cudaFuncSetAttribute(attn_kernel<T, kAttnWarps, kNT>,
+  return cudaFuncSetAttribute(attn_kernel<T, kAttnWarps<kNT>, kNT>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Layout<kAttnWarps, kNT>::kBytes);
+                              Layout<kAttnWarps<kNT>, kNT>::kBytes);
 }
 
 template <typename T, int kNT>
@@ -566,13 +593,13 @@ cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   // request of 4096 (the host's issue included): 20, 14, 11.
   const int64_t slots = 152 * (kNT == 1 ? 3 : 2);
   int cluster = 1;
-  while (cluster < 8 && 2 * cluster * kAttnWarps * (ctas * cluster < slots / 2 ? 1 : 8) <= groups &&
+  while (cluster < 8 && 2 * cluster * kAttnWarps<kNT> * (ctas * cluster < slots / 2 ? 1 : 8) <= groups &&
          ctas * cluster < 3 * slots)
     cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.R) * a.Hkv * cluster, col_groups);
-  cfg.blockDim = dim3(kAttnWarps * 32);
-  cfg.dynamicSmemBytes = Layout<kAttnWarps, kNT>::kBytes;
+  cfg.blockDim = dim3(kAttnWarps<kNT> * 32);
+  cfg.dynamicSmemBytes = Layout<kAttnWarps<kNT>, kNT>::kBytes;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -582,7 +609,7 @@ cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = a.part ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, attn_kernel<T, kAttnWarps, kNT>, a, cluster);
+  return cudaLaunchKernelEx(&cfg, attn_kernel<T, kAttnWarps<kNT>, kNT>, a, cluster);
 }
 
 template <typename T>
