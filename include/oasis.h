@@ -615,16 +615,17 @@ OASIS_API int oasis_profile_read(oasis_ctx* ctx, double* ms_sum4,
  *   page_table  dev [R][max_blocks] int32: the page of each block.
  *   seq_len     dev [R] int32: tokens in the pages, <= 16 * max_blocks; a
  *          request with none (or fewer) is empty.  Entries of the table past
- *          a request's blocks are not read.
+ *          a request's blocks may be anything.
  *   slots       dev [T] int64: 16 * page + token inside the page; negative
  *          slots are skipped.
- * Every call is asynchronous on the caller's stream; none allocates,
- * synchronises or leaves the current device changed, and all may be captured
- * into graphs.  A handle's calls may run on several streams at once as long
- * as none writes pages another one reads.  A bad page, slot or length does
- * not fault: it raises a device error bit (BAD_BLOCK_ID for a table entry or
- * a length, BAD_UNIT for a slot), read by oasis_q8_sync, and the block or
- * token is left out.
+ * The write, read, attention and verification calls are asynchronous on the
+ * caller's stream: none allocates, synchronises or leaves the current device
+ * changed, and each may be captured into a graph.  A handle's calls may run
+ * on several streams at once as long as none writes pages another one reads
+ * (and, for the prefix, each has scratch of its own); one host thread at a
+ * time.  A bad page, slot or length does not fault: it raises a device error
+ * bit (BAD_BLOCK_ID for a table entry or a length, BAD_UNIT for a slot), read
+ * by oasis_q8_sync, and the block or token is left out.
  * ------------------------------------------------------------------------ */
 #define OASIS_BF16 0
 #define OASIS_FP16 1
@@ -655,8 +656,9 @@ OASIS_API const char* oasis_q8_config_error(const oasis_q8_config* cfg);
 OASIS_API int oasis_q8_query_sizes(const oasis_q8_config* cfg, oasis_q8_sizes* out);
 
 /* A handle on the caller's pages (16-byte aligned, lent for its life, not
- * initialised) and workspace; loads the kernels and clears the error word.
- * *out is NULL on failure. */
+ * initialised) and workspace.  Loads the kernels, waits for the device and
+ * clears the error word.  *out is NULL on failure: OASIS_EINVAL for a bad
+ * configuration or a null or misaligned buffer, OASIS_ECUDA, OASIS_ENOMEM. */
 OASIS_API int oasis_q8_init(const oasis_q8_config* cfg, void* pages, void* workspace,
                             oasis_q8** out);
 /* Release the handle (not the caller's buffers; work in flight is not waited
@@ -667,6 +669,9 @@ OASIS_API const char* oasis_q8_last_error(const oasis_q8* q8);
 /* Wait for the device; OASIS_EDEVICE if a kernel raised an error bit since
  * the last call (then cleared; *device_bits receives them when non-NULL). */
 OASIS_API int oasis_q8_sync(oasis_q8* q8, uint32_t* device_bits);
+
+/* oasis_set_wait_limit for this handle's attention calls. */
+OASIS_API int oasis_q8_set_wait_limit(oasis_q8* q8, long long cycles);
 
 /* Round T tokens' keys and values into the pages.  k, v: dev [T][Hkv][d] of
  * `type` (OASIS_BF16, _FP16, _FP32), consecutive tokens k_stride / v_stride
@@ -692,7 +697,8 @@ OASIS_API int oasis_q8_read(oasis_q8* q8, int num_requests, const int32_t* page_
  * (OASIS_BF16 or _FP16).  With causal != 0 the queries are the last S tokens
  * of the request in order: query s sees the first seq_len - (S - 1 - s)
  * tokens; else each sees all seq_len.  A query that sees nothing gives
- * zeros.  S * Hq / Hkv <= 32.  q and out 16-byte aligned. */
+ * zeros.  q and out 16-byte aligned, not overlapping; num_requests <= 65535
+ * and S * R * Hq < 2^31. */
 OASIS_API int oasis_q8_attn(oasis_q8* q8, int num_requests, int num_queries, int causal,
                             const void* q, int type, const int32_t* page_table,
                             const int32_t* seq_len, void* out, void* stream);

@@ -291,8 +291,9 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
         }
       }
     }
+    // No product may outlive its operands and accumulators, either.
     mma_commit(drain);
-    (void)reached(drain, 0);
+    (void)mbar_wait(drain, 0);
   } else {
     // ---- softmax of row `lane` of this warp's quarter of tile t
     const int t = warp >> 2;

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256) read_kernel(const Q8ReadArgs a, int block
   const int h = static_cast<int>(item % a.Hkv);
   const int b = static_cast<int>(item / a.Hkv % blocks);
   const int r = static_cast<int>(item / a.Hkv / blocks);
-  const int len = a.len[r];
+  const int len = max(a.len[r], 0);
   const int page = a.table[static_cast<int64_t>(r) * a.max_blocks + b];
   const int valid = min(len - b * kBlock, kBlock);
   if (b == 0 && h == 0 && lane == 0 && len > 0 && (len - 1) / kBlock >= blocks) raise_error(a.err, kErrBadBlock);

@@ -65,6 +65,7 @@ struct oasis_q8 {
   float scale_log2 = 0.f;
   uint8_t* pages = nullptr;
   uint32_t* err = nullptr;
+  long long wait_limit = kWaitLimitCycles;
   char last_error[256] = "";
 
   int fail(int code, const char* fmt, ...) {
@@ -100,6 +101,8 @@ OASIS_API int oasis_q8_init(const oasis_q8_config* cfg, void* pages, void* works
   if (preload_q8_cache_kernels() != cudaSuccess || preload_q8_attn_kernels() != cudaSuccess ||
       preload_prefix_kernels() != cudaSuccess)
     return OASIS_ECUDA;
+  // The caller's memory may still be written by what it was used for before.
+  if (cudaDeviceSynchronize() != cudaSuccess) return OASIS_ECUDA;
   if (cudaMemset(workspace, 0, 256) != cudaSuccess) return OASIS_ECUDA;
   oasis_q8* q = new (std::nothrow) oasis_q8;
   if (!q) return OASIS_ENOMEM;
@@ -135,6 +138,12 @@ OASIS_API int oasis_q8_sync(oasis_q8* q8, uint32_t* device_bits) {
   if (!bits) return OASIS_OK;
   if (int rc = q8->cuda(cudaMemset(q8->err, 0, sizeof bits), "clear device error word")) return rc;
   return q8->fail(OASIS_EDEVICE, "device error bits 0x%x", bits);
+}
+
+OASIS_API int oasis_q8_set_wait_limit(oasis_q8* q8, long long cycles) {
+  if (!q8) return OASIS_EINVAL;
+  q8->wait_limit = cycles > 0 ? cycles : kWaitLimitCycles;
+  return OASIS_OK;
 }
 
 OASIS_API int oasis_q8_write(oasis_q8* q8, const void* k, const void* v, int type,
@@ -233,7 +242,7 @@ int attn_args(oasis_q8* q8, const char* who, int R, int S, int causal, const voi
   a->type = type;
   a->out_fp32 = q8->cfg.out_fp32;
   a->scale_log2 = q8->scale_log2;
-  a->wait_limit = kWaitLimitCycles;
+  a->wait_limit = q8->wait_limit;
   return OASIS_OK;
 }
 
@@ -333,7 +342,7 @@ OASIS_API int oasis_prefix_attn(oasis_q8* q8, int num_requests, int num_queries,
   p.splits = sh.splits;
   p.out_fp32 = q8->cfg.out_fp32;
   p.scale_log2 = q8->scale_log2;
-  p.wait_limit = kWaitLimitCycles;
+  p.wait_limit = q8->wait_limit;
   const int64_t share = static_cast<int64_t>(sh.splits) * p.Hkv * sh.rows;  // the pages' share
   a.part = p.part + share * kHeadDim;
   a.stat = p.stat + share;

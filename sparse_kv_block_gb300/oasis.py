@@ -148,6 +148,7 @@ EXPORTS = {
     "oasis_q8_destroy": (c_int, [_P]),
     "oasis_q8_last_error": (c_char_p, [_P]),
     "oasis_q8_sync": (c_int, [_P, POINTER(c_uint32)]),
+    "oasis_q8_set_wait_limit": (c_int, [_P, ctypes.c_longlong]),
     "oasis_q8_write": (c_int, [_P, _P, _P, c_int, c_int64, c_int64, _P, c_int, _P]),
     "oasis_q8_read": (c_int, [_P, c_int, _P, _P, _P, c_int, c_int, _P]),
     "oasis_q8_attn": (c_int, [_P, c_int, c_int, c_int, _P, c_int, _P, _P, _P, _P]),
@@ -588,6 +589,8 @@ class Q8Cache:
     uint8 (allocated zeroed unless passed in) and the handle's workspace.
     Methods map one-to-one onto the C ABI calls; tensors of another type,
     shape, device or layout than documented there are refused (ValueError).
+    Calls run on ``stream`` (default: the device's current one); tensors
+    allocated on another stream have to live until it is done with them.
     """
 
     def __init__(self, cfg: oasis_q8_config, pages: Optional[torch.Tensor] = None):
@@ -635,6 +638,11 @@ class Q8Cache:
             raise OasisError(rc, f"device error bits 0x{bits.value:x}")
         self._check(rc)
         return bits.value
+
+    def oasis_q8_set_wait_limit(self, cycles: int) -> None:
+        """Barrier-wait limit of the following attention launches in clock cycles (<= 0: the
+        default, about a second)."""
+        self._check(lib().oasis_q8_set_wait_limit(self.q8, int(cycles)))
 
     def _rows(self, name: str, x: torch.Tensor, T: int, dtype) -> int:
         """Elements between consecutive tokens of x [T][Hkv][d], whose heads are contiguous."""

@@ -510,6 +510,79 @@ def test_python_refusals(dev):
     assert c.oasis_q8_sync() == 0
 
 
+def test_workspace_is_checked(dev):
+    c = cache_of(4, 2, 8, 2)
+    t, n = torch.zeros(1, 2, dtype=torch.int32, device=dev), torch.ones(1, dtype=torch.int32, device=dev)
+    q = torch.zeros(1, 1, 8, 128, dtype=BF, device=dev)
+    kv = torch.zeros(2, 10, 2, 16, 128, dtype=BF, device=dev)
+    ws = c.prefix_workspace(1, 1, 160)
+    assert ws.numel() >= 2 * 4 * (128 * 4 + 8)
+    for bad in (ws[:-1], torch.empty(0, dtype=torch.uint8, device=dev),
+                torch.empty(ws.numel() + 1, dtype=torch.uint8, device=dev)[1:]):
+        with pytest.raises(ob.OasisError) as e:
+            c.oasis_prefix_attn(q, kv, 160, t, n, q.clone(), bad)
+        assert "workspace" in str(e.value)
+    c.oasis_prefix_attn(q, kv, 160, t, n, q.clone(), ws)
+    assert c.oasis_q8_sync() == 0
+    for args in ((1, 5, 3), (1, 0, 3), (-1, 1, 3), (1, 1, -1)):
+        with pytest.raises(ob.OasisError):
+            c.oasis_prefix_workspace(*args)
+    assert c.oasis_prefix_workspace(0, 1, 100) == 0 and c.oasis_prefix_workspace(3, 1, 0) == 0
+
+
+def test_negative_lengths_and_any_entries_behind_a_context(dev):
+    g = gen(25)
+    c = cache_of(10, 6, 8, 2, out_fp32=True)
+    pages = fill(c, g, spread=0.5)
+    lens = [-5, 20, -(1 << 31), 0]
+    table = torch.randint(-(1 << 31), (1 << 31) - 1, (4, 6), generator=g).to(torch.int32)
+    table[1, :2] = torch.tensor([3, 7])
+    q = torch.randn(2, 4, 8, 128, generator=g).to(BF)
+    kv, ref = prefix_of(g, 2, 3, 40)
+    for causal in (False, True):
+        out = attend(c, q.cuda(), table, lens, causal)
+        o, b = Q.attention(q, pages, table.numpy(), lens, causal, out=FP)
+        close(out, o, b)
+        out = attend(c, q.cuda(), table, lens, causal, prefix=kv, plen=40)
+        o, b = Q.attention(q, pages, table.numpy(), lens, causal, prefix=ref, p_half=2.0 ** -8, out=FP)
+        close(out, o, b)
+    back = torch.full((4, 2, 6, 2, 16, 128), 3.0, dtype=FP, device=dev)
+    c.oasis_q8_read(table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), back)
+    assert c.oasis_q8_sync() == 0
+    assert (back[0] == 3).all() and (back[2:] == 3).all() and (back[1, :, 2:] == 3).all()
+
+
+def test_waits_that_run_out_are_reported(dev):
+    """A limit of one cycle, on a pool larger than the L2 cache so that copies are still under way
+    when they are waited for: the calls return, the error bit is raised, and with the default
+    limit the same handle answers as before."""
+    R, n, Hkv, plen = 48, 2048, 8, 8000
+    pages = torch.randint(0, 64, (R * n // 16, Hkv, Q.UNIT), dtype=torch.uint8, device=dev)
+    pages[..., 4096:] = 124
+    assert pages.numel() > 160 << 20
+    c = ob.Q8Cache(ob.make_q8_config(R * n // 16, n // 16, 32, Hkv), pages=pages)
+    g = gen(26)
+    lens = [n] * R
+    table = torch.randperm(R * n // 16, generator=g).to(torch.int32).view(R, n // 16)
+    q = torch.randn(2, R, 32, 128, generator=g).to(BF).cuda()
+    kv = torch.randn(Hkv, plen // 16, 2, 16, 128, device=dev).to(BF)
+
+    def both():
+        return [attend(c, q, table, lens, True), attend(c, q, table, lens, True, prefix=kv, plen=plen)]
+    before = both()
+    assert c.oasis_q8_sync() == 0
+    for prefix in (None, kv):
+        c.oasis_q8_set_wait_limit(1)
+        attend(c, q, table, lens, True, prefix=prefix, plen=plen)
+        with pytest.raises(ob.OasisError) as e:
+            c.oasis_q8_sync()
+        assert e.value.status == ob.OASIS_EDEVICE and "0x2" in str(e.value)
+        c.oasis_q8_set_wait_limit(0)
+        after = both()
+        assert c.oasis_q8_sync() == 0
+        assert all(torch.equal(x, y) for x, y in zip(before, after))
+
+
 # ------------------------------------------------------- streams and graphs
 def test_streams_and_graph_replay(dev):
     """Write and both attentions captured once, replayed on new contents; the same calls on a side

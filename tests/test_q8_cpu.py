@@ -61,6 +61,7 @@ def test_null_and_misaligned_arguments():
     assert L.oasis_prefix_attn(None, 1, 1, 0, 16, 0, 16, 1, 1, 16, 16, 16, None, 0, None) == ob.OASIS_EINVAL
     assert L.oasis_prefix_workspace(None, 1, 1, 1, None) == ob.OASIS_EINVAL
     assert L.oasis_q8_sync(None, None) == ob.OASIS_EINVAL
+    assert L.oasis_q8_set_wait_limit(None, 5) == ob.OASIS_EINVAL
     assert L.oasis_q8_last_error(None) == b"null handle"
     assert L.oasis_q8_destroy(None) == ob.OASIS_OK
     assert L.oasis_verify_drafts(None, None) == ob.OASIS_EINVAL
