@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   uint64_t* drain = o_done + 2;
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
 
-  asm volatile("griddepcontrol.launch_dependents;");  // the pages' share takes the SMs this leaves idle
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_tile = blockIdx.x % a.row_tiles;
   const int h = (blockIdx.x / a.row_tiles) % a.Hkv;
@@ -182,6 +181,9 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
     load_blocks(dst + kHalfTile, &map, 64, j & 1, block, h, &full[st]);
   };
   int loaded = 0;
+  if (warp == kTiles * 4 + 1) tmem_alloc(tmem_s, Lay::kColumns);
+  previous_done();
+  next_may_begin();  // the pages' share takes the SMs this leaves idle
   if (loader) {
     prefetch_tensormap(&map);
     for (int i = 0; i < 2 * kRingStages + 2; ++i) mbar_init(&bars[i], 1);  // to s_full
@@ -191,7 +193,6 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
     fence_barrier_init();
     for (; loaded < 2 * n && loaded < kRingStages; ++loaded) load(loaded);
   }
-  if (warp == kTiles * 4 + 1) tmem_alloc(tmem_s, Lay::kColumns);
   // The query rows: where each begins (one division a row), then half a warp a
   // row, all of a thread's loads in flight, to where the swizzle has them.
   int* begin = reinterpret_cast<int*>(smem + Lay::kRows);
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
       const int rr = r0 + b * kStep;
       const int at = rr < kTiles * kTile ? begin[rr] : -1;
       v[b] = make_uint4(0u, 0u, 0u, 0u);
-      if (at >= 0) v[b] = __ldg(static_cast<const uint4*>(a.q) + static_cast<int64_t>(at) * 16 + ch);
+      if (at >= 0) v[b] = static_cast<const uint4*>(a.q)[static_cast<int64_t>(at) * 16 + ch];
     }
 #pragma unroll
     for (int b = 0; b < kLoads; ++b) {
@@ -422,7 +423,8 @@ __global__ void __launch_bounds__(128) join_kernel(const PrefixArgs a) {
   const int h = static_cast<int>(hr / a.R), r = static_cast<int>(hr % a.R);
   T* out = static_cast<T*>(a.out) +
            ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + c - s * a.G) * kHeadDim + lane * 4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  previous_done();
+  next_may_begin();
   const int shares = a.splits + 1;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, sum = 0.f;
@@ -485,41 +487,17 @@ PrefixShape prefix_shape(int R, int S, int G, int Hkv, int prefix_len) {
   return p;
 }
 
-namespace {
-
-// A launch that may begin while the one before it still runs.
-template <typename... Params, typename... Args>
-cudaError_t launch_beside(void (*kernel)(Params...), unsigned grid, int threads, int smem, cudaStream_t s,
-                          const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-}  // namespace
-
 cudaError_t launch_prefix(const PrefixArgs& a, int tiles, const CUtensorMap& map, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.row_tiles) * a.Hkv * a.splits;
-  if (tiles == 2)
-    prefix_kernel<2><<<grid, PrefixLayout<2>::kThreads, PrefixLayout<2>::kBytes, s>>>(a, map);
-  else
-    prefix_kernel<1><<<grid, PrefixLayout<1>::kThreads, PrefixLayout<1>::kBytes, s>>>(a, map);
-  return cudaGetLastError();
+  return tiles == 2
+             ? launch_early(prefix_kernel<2>, grid, PrefixLayout<2>::kThreads, PrefixLayout<2>::kBytes, s, 0, a, map)
+             : launch_early(prefix_kernel<1>, grid, PrefixLayout<1>::kThreads, PrefixLayout<1>::kBytes, s, 0, a, map);
 }
 
 cudaError_t launch_join(const PrefixArgs& a, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.Hkv) * a.R * a.S * a.G;
   const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  return a.out_fp32 ? launch_beside(join_kernel<float>, grid, 128, 0, s, a)
-                    : launch_beside(join_kernel<__nv_bfloat16>, grid, 128, 0, s, a);
+  return launch_early(a.out_fp32 ? join_kernel<float> : join_kernel<__nv_bfloat16>, grid, 128, 0, s, 0, a);
 }
 
 cudaError_t preload_prefix_kernels() {

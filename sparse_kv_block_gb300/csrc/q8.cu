@@ -20,11 +20,11 @@ template <typename T>
 __device__ __forceinline__ Raw<T> load4(const T* p) {
   Raw<T> r;
   if constexpr (sizeof(T) == 4)
-    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r.w.x), "=r"(r.w.y), "=r"(r.w.z), "=r"(r.w.w)
                  : "l"(p));
   else
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.w.x), "=r"(r.w.y) : "l"(p));
+    asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(r.w.x), "=r"(r.w.y) : "l"(p));
   return r;
 }
 __device__ __forceinline__ float4 floats(const Raw<float>& r) {
@@ -91,6 +91,8 @@ constexpr int kWriteWarps = 4;
 template <typename T, int kSpan>
 __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 4 ? 5 : 7) write_kernel(const Q8WriteArgs a) {
   static_assert(kSpan <= kBlock, "a run from the span's last place ends within 32 lanes");
+  previous_done();
+  next_may_begin();
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int64_t spans = (static_cast<int64_t>(a.T) + kSpan - 1) / kSpan;
@@ -199,6 +201,8 @@ __device__ __forceinline__ void put4(T* p, uint32_t codes, float s) {
 // in registers).  Bound by memory, mostly by what it writes.
 template <typename T>
 __global__ void __launch_bounds__(256) read_kernel(const Q8ReadArgs a, int blocks) {
+  previous_done();
+  next_may_begin();
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (item >= static_cast<int64_t>(a.R) * blocks * a.Hkv) return;
@@ -219,16 +223,16 @@ __global__ void __launch_bounds__(256) read_kernel(const Q8ReadArgs a, int block
            lane * 4;
   uint32_t k[kBlock], v[kBlock];
 #pragma unroll
-  for (int j = 0; j < kBlock; ++j) k[j] = __ldg(reinterpret_cast<const uint32_t*>(unit + q8_key_at(j, lane * 4)));
+  for (int j = 0; j < kBlock; ++j) k[j] = *reinterpret_cast<const uint32_t*>(unit + q8_key_at(j, lane * 4));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(unit + q8_value_at(0, lane * 4 + i)));
+    const uint4 w = *reinterpret_cast<const uint4*>(unit + q8_value_at(0, lane * 4 + i));
     v[i] = w.x;
     v[4 + i] = w.y;
     v[8 + i] = w.z;
     v[12 + i] = w.w;
   }
-  const float scale = pow2f(__ldg(unit + kQ8ExpOffset + lane) - 127);  // lane: key, then value exponents
+  const float scale = pow2f(unit[kQ8ExpOffset + lane] - 127);  // lane: key, then value exponents
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     uint32_t w[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
@@ -260,9 +264,7 @@ cudaError_t launch_write(const Q8WriteArgs& a, cudaStream_t s) {
   const bool one = rows < 152 * 64;
   const int64_t items = one ? rows : (static_cast<int64_t>(a.T) + kLongSpan - 1) / kLongSpan * a.Hkv * 2;
   const unsigned grid = static_cast<unsigned>((items + kWriteWarps - 1) / kWriteWarps);
-  if (one) write_kernel<T, 1><<<grid, kWriteWarps * 32, 0, s>>>(a);
-  else write_kernel<T, kLongSpan><<<grid, kWriteWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(one ? write_kernel<T, 1> : write_kernel<T, kLongSpan>, grid, kWriteWarps * 32, 0, s, 0, a);
 }
 
 template <typename T>
@@ -270,8 +272,7 @@ cudaError_t launch_read(const Q8ReadArgs& a, cudaStream_t s) {
   const int blocks = a.max_blocks < a.out_blocks ? a.max_blocks : a.out_blocks;
   const int64_t items = static_cast<int64_t>(a.R) * blocks * a.Hkv;
   if (items == 0) return cudaSuccess;
-  read_kernel<T><<<static_cast<unsigned>((items + 7) / 8), 256, 0, s>>>(a, blocks);
-  return cudaGetLastError();
+  return launch_early(read_kernel<T>, static_cast<unsigned>((items + 7) / 8), 256, 0, s, 0, a, blocks);
 }
 
 template <typename T>

@@ -77,6 +77,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// ---- launches that overlap (see launch_early)
+// Wait until the launch ahead in the stream has ended and its writes are seen.
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The launch behind may begin (when all CTAs have said so).
+__device__ __forceinline__ void next_may_begin() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ---- parts of a softmax, each (outputs, sum) in units of 2^m
 // 2^(m - mx); where no part has seen a score (mx = -inf) the parts are zeros,
 // or NaN, and are added as they are.

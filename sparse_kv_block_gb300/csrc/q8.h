@@ -85,6 +85,30 @@ struct VerifyArgs {
   int R, n, V, type;
 };
 
+// A launch that may begin before the one ahead of it in the stream has ended
+// (programmatic dependent launch).  Its kernel waits for that one, with
+// previous_done(), before it touches memory; only the launches of one prefix
+// attention wait later, where they say so.  In a loop of small calls this
+// hides most of a launch.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         int cluster, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_q8_write(const Q8WriteArgs& a, cudaStream_t s);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
 cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s);

@@ -78,7 +78,11 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
   using Lay = Layout<W, kNT>;
   constexpr int kCols = Lay::kCols;
   extern __shared__ __align__(128) uint8_t smem[];
-  if (a.part) asm volatile("griddepcontrol.launch_dependents;");  // the join may begin
+  // A prefix's share of pages needs nothing of the launch ahead, the prefix's
+  // own, which has itself waited for what came before.  (This grid has not:
+  // it reads past L1, which may hold what was there before.)
+  if (!a.part) previous_done();
+  next_may_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int pair = blockIdx.x / cluster;
@@ -104,9 +108,9 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
   const int32_t* row = a.table + static_cast<int64_t>(r) * a.max_blocks;
   auto page_of = [&](int k) {
     const int64_t b = (first + static_cast<int64_t>(k) * step) * kGroupUnits + lane;
-    return lane < kGroupUnits && b < a.max_blocks ? __ldg(row + b) : -1;
+    return lane < kGroupUnits && b < a.max_blocks ? __ldcg(row + b) : -1;
   };
-  int len = __ldg(a.len + r);
+  int len = __ldcg(a.len + r);
   int page = page_of(0);
   uint4 qv[4];  // warp nt < kNT: of column 8 nt + g, dims 64 (j / 2) + 16 t + 8 (j % 2) .. + 7
   {
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
           static_cast<const T*>(a.q) +
           ((static_cast<int64_t>(c / a.G) * a.R + r) * a.Hq + h * a.G + c % a.G) * kHeadDim);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) qv[j] = __ldg(src + (j >> 1) * 8 + t * 2 + (j & 1));
+      for (int j = 0; j < 4; ++j) qv[j] = __ldcg(src + (j >> 1) * 8 + t * 2 + (j & 1));
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) qv[j] = make_uint4(0u, 0u, 0u, 0u);
@@ -564,21 +568,17 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
   // have waited for that one.  One CTA does it for all (others would keep SMs
   // from the CTAs behind them).
   if (a.part && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    previous_done();
   if (cluster == 1) return;
   cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
-#ifndef W2
-#define W2 4
-#endif
-template <int kNT>
-constexpr int kAttnWarps = kNT == 1 ? 4 : W2;
+constexpr int kAttnWarps = 4;
 
 template <typename T, int kNT>
 cudaError_t configure() {
-  return cudaFuncSetAttribute(attn_kernel<T, kAttnWarps<kNT>, kNT>,
+  return cudaFuncSetAttribute(attn_kernel<T, kAttnWarps, kNT>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Layout<kAttnWarps<kNT>, kNT>::kBytes);
+                              Layout<kAttnWarps, kNT>::kBytes);
 }
 
 template <typename T, int kNT>
@@ -593,23 +593,12 @@ cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   // request of 4096 (the host's issue included): 20, 14, 11.
   const int64_t slots = 152 * (kNT == 1 ? 3 : 2);
   int cluster = 1;
-  while (cluster < 8 && 2 * cluster * kAttnWarps<kNT> * (ctas * cluster < slots / 2 ? 1 : 8) <= groups &&
+  while (cluster < 8 && 2 * cluster * kAttnWarps * (ctas * cluster < slots / 2 ? 1 : 8) <= groups &&
          ctas * cluster < 3 * slots)
     cluster *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.R) * a.Hkv * cluster, col_groups);
-  cfg.blockDim = dim3(kAttnWarps<kNT> * 32);
-  cfg.dynamicSmemBytes = Layout<kAttnWarps<kNT>, kNT>::kBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // beside the prefix's launch
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = a.part ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, attn_kernel<T, kAttnWarps<kNT>, kNT>, a, cluster);
+  return launch_early(attn_kernel<T, kAttnWarps, kNT>,
+                      dim3(static_cast<unsigned>(a.R) * a.Hkv * cluster, col_groups), kAttnWarps * 32,
+                      Layout<kAttnWarps, kNT>::kBytes, s, cluster, a, cluster);
 }
 
 template <typename T>

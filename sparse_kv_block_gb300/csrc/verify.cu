@@ -19,7 +19,7 @@
 // distributed shared memory, each finds the segment that the threshold falls
 // in, and the CTA that read it reads those entries again, all its threads
 // together.  No scratch in global memory, one launch.
-#include "common.cuh"
+#include "q8.cuh"
 #include "q8.h"
 
 #include <cuda_fp16.h>
@@ -43,9 +43,9 @@ template <typename T, bool kVec>
 __device__ __forceinline__ float4 row4(const T* p, int at, int V) {
   if (kVec && at + 4 <= V) {
     if constexpr (sizeof(T) == 4) {
-      return __ldg(reinterpret_cast<const float4*>(p + at));
+      return *reinterpret_cast<const float4*>(p + at);
     } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p + at));
+      const uint2 w = *reinterpret_cast<const uint2*>(p + at);
       T t[4];
       memcpy(t, &w, 8);
       return make_float4(to_f(t[0]), to_f(t[1]), to_f(t[2]), to_f(t[3]));
@@ -141,6 +141,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   __shared__ int first_s, bad_s, seg_s, last_s;
   __shared__ Pair target_s;            // the threshold, from its segment's start
   __shared__ Pair warp_sum[kVerifyWarps];
+  previous_done();
+  next_may_begin();
   const int r = blockIdx.x / cluster;
   const int rank = static_cast<int>(cluster_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -328,21 +330,9 @@ cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
   const int segs = brief ? (a.V + kShortSeg - 1) / kShortSeg : longs;
   int cluster = 1;
   while (cluster < 8 && cluster * kVerifyWarps < segs && 2 * cluster * a.R <= 2 * 152) cluster *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.R) * cluster);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  if (brief)
-    return vec ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true, kShortSeg>, a, cluster)
-               : cudaLaunchKernelEx(&cfg, verify_kernel<T, false, kShortSeg>, a, cluster);
-  return vec ? cudaLaunchKernelEx(&cfg, verify_kernel<T, true, kLongSeg>, a, cluster)
-             : cudaLaunchKernelEx(&cfg, verify_kernel<T, false, kLongSeg>, a, cluster);
+  const auto kernel = brief ? (vec ? verify_kernel<T, true, kShortSeg> : verify_kernel<T, false, kShortSeg>)
+                            : (vec ? verify_kernel<T, true, kLongSeg> : verify_kernel<T, false, kLongSeg>);
+  return launch_early(kernel, static_cast<unsigned>(a.R) * cluster, kThreads, 0, s, cluster, a, cluster);
 }
 
 template <typename T>

@@ -624,6 +624,56 @@ def test_streams_and_graph_replay(dev):
     assert c.oasis_q8_sync() == 0
 
 
+def test_calls_in_a_row_see_what_the_ones_before_wrote(dev):
+    """Launches may begin before the one ahead has ended: every call of a long run without waiting
+    gives what it gives when each is waited for."""
+    g = gen(33)
+    N, R = 60, 40
+    c = cache_of(R * 4, 4, 8, 2)
+    table = torch.randperm(R * 4, generator=g).to(torch.int32).view(R, 4).cuda()
+    lens = torch.randint(30, 61, (R,), generator=g)
+    slots = torch.stack([Q.slots_of(table.cpu(), r, m - 1, m)[0] for r, m in enumerate(lens.tolist())]).cuda()
+    ks, vs = torch.randn(2, N, R, 2, 128, generator=g).to(BF).cuda()
+    qs = torch.randn(N, 2, R, 8, 128, generator=g).to(BF).cuda()
+    kv, _ = prefix_of(g, 2, 20, 310)
+    ws = c.prefix_workspace(R, 2, 310)
+    q, k, v = torch.zeros_like(qs[0]), torch.zeros_like(ks[0]), torch.zeros_like(vs[0])
+    n = torch.zeros(R, dtype=torch.int32, device=dev)
+    n_all = lens.to(torch.int32).cuda()
+
+    def go(wait):
+        c.pages.zero_()
+        fill_k = torch.arange(R * 64, device=dev)
+        c.oasis_q8_write(base, base, fill_k)
+        out = torch.zeros(N, 3, *q.shape, dtype=BF, device=dev)
+        back = torch.zeros(N, R, 2, 4, 2, 16, 128, dtype=BF, device=dev)
+        w = torch.cuda.synchronize if wait else lambda: None
+        for i in range(N):
+            for a, b in ((q, qs[i]), (k, ks[i]), (v, vs[i]), (n, n_all - i % 3)):
+                a.copy_(b)
+                w()
+            c.oasis_q8_write(k, v, slots)
+            w()
+            c.oasis_q8_attn(q, table, n, out[i, 0], causal=True)
+            w()
+            c.oasis_prefix_attn(q, kv, 310, table, n, out[i, 1], ws)
+            w()
+            c.oasis_q8_attn(out[i, 1], table, n, out[i, 2])        # reads what the call before wrote
+            w()
+            c.oasis_q8_read(table, n, back[i])
+            w()
+            q.zero_(), n.zero_()
+        torch.cuda.synchronize()
+        return out, back
+
+    base = torch.randn(R * 64, 2, 128, generator=g).to(BF).cuda()
+    want = go(True)
+    for _ in range(3):
+        got = go(False)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert float(want[0].abs().sum()) > 0
+
+
 def test_two_prefix_calls_at_once_with_scratch_of_their_own(dev):
     g = gen(32)
     c = cache_of(30, 10, 8, 2)
