@@ -1,5 +1,7 @@
 // q8.cu -- writing keys and values into the 8-bit paged cache, and reading
 // them back.
+#include <type_traits>
+
 #include "q8.cuh"
 #include "q8.h"
 
@@ -40,18 +42,38 @@ __device__ __forceinline__ float4 floats(const Raw<__half>& r) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// |x| of a finite x, else 0 (an infinity or NaN does not set the scale).
+// The warp's largest |x| of a row, as its type's bits without the sign
+// (16-bit types two at a time).
+template <typename T>
+__device__ __forceinline__ uint32_t row_max(const Raw<T>& r) {
+  uint32_t m;
+  if constexpr (sizeof(T) == 4) {
+    m = max(max(r.w.x & 0x7fffffffu, r.w.y & 0x7fffffffu), max(r.w.z & 0x7fffffffu, r.w.w & 0x7fffffffu));
+  } else {
+    const uint32_t two = __vmaxu2(r.w.x & 0x7fff7fffu, r.w.y & 0x7fff7fffu);
+    m = max(two >> 16, two & 0xffffu);
+  }
+  return __reduce_max_sync(0xffffffffu, m);
+}
+// Such a maximum's fp32 bits; an infinity or NaN gives 0x7f800000 or more.
+template <typename T>
+__device__ __forceinline__ uint32_t float_bits(uint32_t m) {
+  if constexpr (sizeof(T) == 4) return m;
+  if constexpr (std::is_same_v<T, __half>)
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(m))));
+  return m << 16;
+}
+// The fp32 bits of the largest |x| of finite x: infinities and NaN do not set
+// a row's scale.
 __device__ __forceinline__ uint32_t finite_abs_bits(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
   return b < 0x7f800000u ? b : 0u;
 }
-
-// A warp's row of 128 values, four a lane: its exponent and the lane's codes.
-__device__ __forceinline__ uint32_t quantise_row(float4 x, int& e) {
-  const uint32_t m = max(max(finite_abs_bits(x.x), finite_abs_bits(x.y)),
-                         max(finite_abs_bits(x.z), finite_abs_bits(x.w)));
-  e = q8_exponent(__reduce_max_sync(0xffffffffu, m));
-  const float s = pow2f(-e);
+__device__ __forceinline__ uint32_t finite_row_max(float4 x) {
+  return __reduce_max_sync(0xffffffffu, max(max(finite_abs_bits(x.x), finite_abs_bits(x.y)),
+                                            max(finite_abs_bits(x.z), finite_abs_bits(x.w))));
+}
+__device__ __forceinline__ uint32_t codes_of(float4 x, float s) {
   return q8_pack4(x.x * s, x.y * s, x.z * s, x.w * s);
 }
 
@@ -78,8 +100,10 @@ constexpr int kWriteWarps = 4;
 // bytes written a token and head.  What holds it back is latency (the slots,
 // then the rows): 16 rows a warp are asked for at once, and seven CTAs of
 // four warps an SM were the best of what registers allow (32768 tokens x 8
-// heads, bf16: 39.6 us = 5.1 TB/s; six 42, eight 41, nine 48, ten 50; CTAs of
-// eight warps 43 to 53).
+// heads, bf16: 39.6 us, six 42, eight 41, nine 48, ten 50; CTAs of eight warps
+// 43 to 53).  Then integer work (70 % of its pipe): maxima of two 16-bit
+// values at a time 35.8 us, a row's exponent made by one lane 35.0 us = 5.8
+// TB/s.
 //
 // Values are stored with a block's tokens consecutive, so single tokens mean
 // single bytes 16 apart; whole blocks are worth finding.  The tokens are cut
@@ -129,12 +153,27 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 4 ? 5 : 7) writ
       Raw<T> v[kBlock];
 #pragma unroll
       for (int i = 0; i < kBlock; ++i) v[i] = load4(x + i * stride);
+      // Lane i makes row i's exponent and scale (the whole warp doing each
+      // row's would double the integer work, which is what fills the SM).
+      uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < kBlock; ++i) {
-        int e;
-        codes[i] = quantise_row(floats(v[i]), e);
-        if (lane == i) mine = e;
+        const uint32_t m = row_max(v[i]);
+        if (lane == i) top = m;
       }
+      top = float_bits<T>(top);
+      if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {
+          const uint32_t m = finite_row_max(floats(v[i]));
+          if (lane == i) top = m;
+        }
+      }
+      mine = q8_exponent(top);
+      const float scale = pow2f(-mine);
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i)
+        codes[i] = codes_of(floats(v[i]), __shfl_sync(0xffffffffu, scale, i));
       if (values) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -157,8 +196,9 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 4 ? 5 : 7) writ
       }
     } else {
       for (int i = 0; i < n; ++i) {
-        int e;
-        const uint32_t c = quantise_row(floats(load4(x + i * stride)), e);
+        const float4 f = floats(load4(x + i * stride));
+        const int e = q8_exponent(finite_row_max(f));
+        const uint32_t c = codes_of(f, pow2f(-e));
         if (lane == i) mine = e;
         if (values) {
 #pragma unroll
