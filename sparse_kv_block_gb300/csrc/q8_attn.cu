@@ -74,7 +74,7 @@ __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 
 template <typename T, int W, int kNT>
 __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
-    attn_kernel(const Q8AttnArgs a, int cluster) {
+    attn_kernel(const Q8AttnArgs a, int most, int each) {
   using Lay = Layout<W, kNT>;
   constexpr int kCols = Lay::kCols;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
   next_may_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int pair = blockIdx.x / cluster;
-  const int rank = static_cast<int>(cluster == 1 ? 0u : cluster_rank());
+  const int pair = blockIdx.x / most;
+  const int rank = static_cast<int>(most == 1 ? 0u : cluster_rank());
   const int r = pair / a.Hkv, h = pair - r * a.Hkv;
   const int col0 = blockIdx.y * kCols;                 // first column of this CTA
   const int cols = min(a.S * a.G - col0, kCols);
@@ -104,8 +104,9 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
 
   // Loads that need nothing else, in flight together: the length, the first
   // group's pages (rows of the table are readable throughout) and the queries.
-  const int first = rank * W + warp, step = cluster * W;
+  const int first = rank * W + warp;
   const int32_t* row = a.table + static_cast<int64_t>(r) * a.max_blocks;
+  int step = 0;  // groups between a warp's, once the length is known
   auto page_of = [&](int k) {
     const int64_t b = (first + static_cast<int64_t>(k) * step) * kGroupUnits + lane;
     return lane < kGroupUnits && b < a.max_blocks ? __ldcg(row + b) : -1;
@@ -132,6 +133,14 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
     len = a.max_blocks * kBlock;
   }
   const int groups = (len + kGroupTokens - 1) / kGroupTokens;
+  // A request takes as many of the cluster's CTAs as have `each` groups a warp
+  // (one for a short one); the others leave at once.
+  const int cluster = min(most, max((groups + W * each - 1) / (W * each), 1));
+  if (rank >= cluster) {
+    if (a.part && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) previous_done();  // see the end
+    return;
+  }
+  step = cluster * W;
   const int count = groups > first ? (groups - first + step - 1) / step : 0;
 
   // Lanes 0..3 fetch a group's pages (the table's entries a turn ahead) and
@@ -585,20 +594,28 @@ template <typename T, int kNT>
 cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   const int64_t ctas = static_cast<int64_t>(a.R) * a.Hkv * col_groups;
   const int groups = (a.max_blocks + kGroupUnits - 1) / kGroupUnits;
-  // CTAs of a pair: while the card is not full, as many as have a group for
-  // every warp; beyond that up to about three rounds of CTAs (the last round's
-  // idle SMs), each warp keeping eight groups or more to spread its start and
-  // join over.  GB300, 64 requests x 8 heads x 16384 tokens, two queries: 350
-  // us at two, 325 at four, 350 at eight; 32 x 8 x 8192: 123, 108, 115; one
-  // request of 4096 (the host's issue included): 20, 14, 11.
+  // CTAs of a pair, by the longest context that the table can hold.  While
+  // all fit the card at once: as many as have a group for every warp (latency
+  // counts: one request of 4096 tokens takes 27.6, 17.0, 11.1, 8.3 us with
+  // one, two, four, eight).  Beyond that, where every warp keeps eight groups
+  // to spread its start and join over: up to three rounds of CTAs, or one and
+  // a half with two column tiles (two CTAs an SM), so that long requests do
+  // not run on alone.  GB300, us with one, two, four, eight: 64 requests x 8
+  // heads x 16384 tokens 402, 338, 316, 338; 24 ragged ones up to 9001, four
+  // queries 94, 71, 71, 87; 10 x 16 heads up to 20000 129, 96, 65, 72; but 32
+  // even ones of 8192 89, 111, 98, 104.  Short contexts stay whole: 64 up to
+  // 2000 33, 39, 45, 56.
   const int64_t slots = 152 * (kNT == 1 ? 3 : 2);
-  int cluster = 1;
-  while (cluster < 8 && 2 * cluster * kAttnWarps * (ctas * cluster < slots / 2 ? 1 : 8) <= groups &&
-         ctas * cluster < 3 * slots)
+  const int64_t enough = kNT == 1 ? 3 * slots : slots * 3 / 2;
+  int cluster = 1, each = 1;
+  while (cluster < 8 && ctas * cluster * 2 <= slots && 2 * cluster * kAttnWarps <= groups) cluster *= 2;
+  while (cluster < 8 && ctas * cluster < enough && 2 * cluster * kAttnWarps * 8 <= groups) {
     cluster *= 2;
+    each = ctas * cluster > slots ? 6 : 1;
+  }
   return launch_early(attn_kernel<T, kAttnWarps, kNT>,
                       dim3(static_cast<unsigned>(a.R) * a.Hkv * cluster, col_groups), kAttnWarps * 32,
-                      Layout<kAttnWarps, kNT>::kBytes, s, cluster, a, cluster);
+                      Layout<kAttnWarps, kNT>::kBytes, s, cluster, a, cluster, each);
 }
 
 template <typename T>
