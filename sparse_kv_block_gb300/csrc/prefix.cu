@@ -69,26 +69,32 @@ constexpr uint32_t kInstrBt = kInstr | 1u << 16;
 // the warp's alike stay in uniform registers, where the instruction wants
 // them.  (From a branch of one lane each product took 70 cycles to issue,
 // more than the 64 it runs.)
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t add) {
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t add, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kInstr), "r"(add)
+      "l"(a), "l"(b), "r"(kInstr), "r"(add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t add, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kInstrBt), "r"(add)
+      "r"(a), "l"(b), "r"(kInstrBt), "r"(add), "r"(lead)
       : "memory");
 }
 // Arrive on `bar` when the elected lane's products so far are done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_u32(bar))
+          smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 __device__ __forceinline__ void fence_before() {
@@ -151,7 +157,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   uint64_t* full = bars;                       // [4] a stage has landed
   uint64_t* empty = bars + kRingStages;        // [4] its products are done
   uint64_t* s_full = bars + 2 * kRingStages;   // [2] scores of a tile
-  uint64_t* p_half = s_full + 2;               // [2] its first 64 tokens' weights (128 threads)
+  uint64_t* p_half = s_full + 2;               // [2] its first 64 tokens' weights (four warps)
   uint64_t* p_full = p_half + 2;               // [2] all its weights
   uint64_t* o_done = p_full + 2;               // [2] its outputs
   uint64_t* drain = o_done + 2;
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   if (loader) {
     prefetch_tensormap(&map);
     for (int i = 0; i < 2 * kRingStages + 2; ++i) mbar_init(&bars[i], 1);  // to s_full
-    for (int i = 0; i < 4; ++i) mbar_init(&p_half[i], 128);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_half[i], 4);
     for (int i = 0; i < 2; ++i) mbar_init(&o_done[i], 1);
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -243,6 +249,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
     }
   } else if (warp == kTiles * 4 + 1) {
     // ---- products
+    const uint32_t lead = elected();
     auto reached = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, a.wait_limit)) != 0;
     };
@@ -257,10 +264,10 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
       for (int s = 0; s < 8; ++s) {  // 16 dims a step
         constexpr int kHalf = kHalfTile >> 4;
         const uint32_t off = (s >> 2) * kHalf + (s & 3) * 2;
-        mma_ss(tmem + t * 128, q + off, k + off, s > 0);
+        mma_ss(tmem + t * 128, q + off, k + off, s > 0, lead);
       }
-      mma_commit(&s_full[t]);
-      if (t == kTiles - 1) mma_commit(&empty[(2 * i) % kRingStages]);
+      mma_commit(&s_full[t], lead);
+      if (t == kTiles - 1) mma_commit(&empty[(2 * i) % kRingStages], lead);
     };
     ok = landed(0);
     if (ok) {
@@ -280,11 +287,12 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
           fence_after();
 #pragma unroll
           for (int s = half * 4; s < half * 4 + 4; ++s)  // 16 tokens a step
-            mma_ts(tmem + kTiles * 128 + t * 128, tmem + t * 128 + s * 8, v + s * (16 * 128 >> 4), i > 0 || s > 0);
+            mma_ts(tmem + kTiles * 128 + t * 128, tmem + t * 128 + s * 8, v + s * (16 * 128 >> 4), i > 0 || s > 0,
+                   lead);
         }
         if (!ok) break;
-        mma_commit(&o_done[t]);
-        if (t == kTiles - 1) mma_commit(&empty[(2 * i + 1) % kRingStages]);
+        mma_commit(&o_done[t], lead);
+        if (t == kTiles - 1) mma_commit(&empty[(2 * i + 1) % kRingStages], lead);
         if (i + 1 < n) {
           if (t == 0) ok = landed(2 * i + 2);
           if (!ok) break;
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
       }
     }
     // No product may outlive its operands and accumulators, either.
-    mma_commit(drain);
+    mma_commit(drain, lead);
     (void)mbar_wait(drain, 0);
   } else {
     // ---- softmax of row `lane` of this warp's quarter of tile t
@@ -377,7 +385,8 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
         tmem_st32(s_at + c * 32, w);
         tmem_wait_st();
         fence_before();
-        mbar_arrive(c ? &p_full[t] : &p_half[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c ? &p_full[t] : &p_half[t]);  // one a warp: arrivals queue
       }
       l += f2sum(fadd2(sum[0], sum[1]));
     }
