@@ -41,8 +41,8 @@ struct Layout {
   static constexpr int kCols = 8 * kNT;
   static constexpr int kRing = W * kGroupBytes;              // one group a warp
   static constexpr int kPartial = kCols * kHeadDim * 4;      // one warp's partial output
-  static_assert((W + 1) * kPartial + 3 * kCols * 4 <= kRing, "the partial outputs reuse the ring");
-  static constexpr int kMerged = W * kPartial;               // the CTA's [kCols][d], then [kCols] M, L, sums
+  static_assert(W * kPartial + (W > 1 ? kPartial + 3 * kCols * 4 : 0) <= kRing, "the partial outputs reuse the ring");
+  static constexpr int kMerged = W * kPartial;               // (W > 1) the CTA's [kCols][d], [kCols] M, L, sums
   static constexpr int kBars = kRing;                        // keys' and values' barrier a warp
   static constexpr int kValid = kBars + W * 16;              // int4 for even and odd groups
   static constexpr int kStat = kValid + W * 32;              // [W][kCols] M, L, sums
@@ -73,7 +73,7 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 
 template <typename T, int W, int kNT>
-__global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
     attn_kernel(const Q8AttnArgs a, int most, int each) {
   using Lay = Layout<W, kNT>;
   constexpr int kCols = Lay::kCols;
@@ -581,16 +581,14 @@ __global__ void __launch_bounds__(W * 32, kNT == 1 ? 3 : 2)
   if (cluster == 1) return;
   cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
-constexpr int kAttnWarps = 4;
-
-template <typename T, int kNT>
+template <typename T, int W, int kNT>
 cudaError_t configure() {
-  return cudaFuncSetAttribute(attn_kernel<T, kAttnWarps, kNT>,
+  return cudaFuncSetAttribute(attn_kernel<T, W, kNT>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Layout<kAttnWarps, kNT>::kBytes);
+                              Layout<W, kNT>::kBytes);
 }
 
-template <typename T, int kNT>
+template <typename T, int W, int kNT>
 cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   const int64_t ctas = static_cast<int64_t>(a.R) * a.Hkv * col_groups;
   const int groups = (a.max_blocks + kGroupUnits - 1) / kGroupUnits;
@@ -605,24 +603,37 @@ cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   // queries 94, 71, 71, 87; 10 x 16 heads up to 20000 129, 96, 65, 72; but 32
   // even ones of 8192 89, 111, 98, 104.  Short contexts stay whole: 64 up to
   // 2000 33, 39, 45, 56.
-  const int64_t slots = 152 * (kNT == 1 ? 3 : 2);
+  const int64_t slots = 152 * ((kNT == 1 ? 12 : 8) / W);
   const int64_t enough = kNT == 1 ? 3 * slots : slots * 3 / 2;
   int cluster = 1, each = 1;
-  while (cluster < 8 && ctas * cluster * 2 <= slots && 2 * cluster * kAttnWarps <= groups) cluster *= 2;
-  while (cluster < 8 && ctas * cluster < enough && 2 * cluster * kAttnWarps * 8 <= groups) {
+  while (W > 1 && cluster < 8 && ctas * cluster * 2 <= slots && 2 * cluster * W <= groups) cluster *= 2;
+  while (W > 1 && cluster < 8 && ctas * cluster < enough && 2 * cluster * W * 8 <= groups) {
     cluster *= 2;
     each = ctas * cluster > slots ? 6 : 1;
   }
-  return launch_early(attn_kernel<T, kAttnWarps, kNT>,
-                      dim3(static_cast<unsigned>(a.R) * a.Hkv * cluster, col_groups), kAttnWarps * 32,
-                      Layout<kAttnWarps, kNT>::kBytes, s, cluster, a, cluster, each);
+  return launch_early(attn_kernel<T, W, kNT>,
+                      dim3(static_cast<unsigned>(a.R) * a.Hkv * cluster, col_groups), W * 32,
+                      Layout<W, kNT>::kBytes, s, cluster, a, cluster, each);
 }
 
 template <typename T>
 cudaError_t launch_n(const Q8AttnArgs& a, cudaStream_t s) {
-  const int cols = a.S * a.G;
-  if (cols <= 8) return launch_t<T, 1>(a, 1, s);
-  return launch_t<T, 2>(a, (cols + 15) / 16, s);
+  // Warps a CTA: four; where there are more pairs than the card holds such
+  // CTAs, two for contexts up to 512 tokens and (one column tile) one up to
+  // 256: a warp's start and join, some 5 us, are then spread over more of its
+  // 1.4 us groups.  GB300, us with four, two, one: 128 requests x 8 heads x 256
+  // tokens 15.7, 15.5, 13.3; 300 x 16 x 100 66, 41, 37; 128 ragged ones up to
+  // 500 23.3, 23.1, 24.4; with two tiles, 128 up to 300 40, 33; but 64 up to
+  // 1000 19.8, 23.8.
+  const int cols = a.S * a.G, groups = (a.max_blocks + kGroupUnits - 1) / kGroupUnits;
+  const int64_t pairs = static_cast<int64_t>(a.R) * a.Hkv;
+  if (cols <= 8) {
+    if (pairs <= 3 * 152 || groups > 8) return launch_t<T, 4, 1>(a, 1, s);
+    return groups > 4 ? launch_t<T, 2, 1>(a, 1, s) : launch_t<T, 1, 1>(a, 1, s);
+  }
+  const int col_groups = (cols + 15) / 16;
+  if (pairs * col_groups <= 2 * 152 || groups > 8) return launch_t<T, 4, 2>(a, col_groups, s);
+  return launch_t<T, 2, 2>(a, col_groups, s);
 }
 
 }  // namespace
@@ -632,13 +643,22 @@ cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s) {
   return a.type == kBf16 ? launch_n<__nv_bfloat16>(a, s) : launch_n<__half>(a, s);
 }
 
+namespace {
+template <typename T>
+cudaError_t configure_all() {
+  cudaError_t e = configure<T, 4, 1>();
+  if (e == cudaSuccess) e = configure<T, 2, 1>();
+  if (e == cudaSuccess) e = configure<T, 1, 1>();
+  if (e == cudaSuccess) e = configure<T, 4, 2>();
+  if (e == cudaSuccess) e = configure<T, 2, 2>();
+  return e;
+}
+}  // namespace
+
 // Their code and shared memory on the current device.
 cudaError_t preload_q8_attn_kernels() {
-  cudaError_t e = configure<__nv_bfloat16, 1>();
-  if (e == cudaSuccess) e = configure<__nv_bfloat16, 2>();
-  if (e == cudaSuccess) e = configure<__half, 1>();
-  if (e == cudaSuccess) e = configure<__half, 2>();
-  return e;
+  const cudaError_t e = configure_all<__nv_bfloat16>();
+  return e == cudaSuccess ? configure_all<__half>() : e;
 }
 
 }  // namespace oasis
