@@ -106,15 +106,54 @@ constexpr int kWriteWarps = 4;
 // TB/s.
 //
 // Values are stored with a block's tokens consecutive, so single tokens mean
-// single bytes 16 apart; whole blocks are worth finding.  The tokens are cut
-// into runs: a run begins where the slot is not the one before plus one, or
-// is a block's first, and so holds at most a block.  A warp takes kSpan
-// tokens' places, one head and keys or values, and treats every run that
-// begins there, reading on past its span where the run does; a run that is a
-// whole block is transposed in registers and stored in whole sectors.
+// single bytes 16 apart; whole blocks (16 consecutive slots from a block's
+// first, wherever in the call they begin) are worth finding.  A warp takes 16
+// consecutive tokens, one head and keys or values; it treats the whole blocks
+// that begin among them, reading on past its tokens where they do, transposed
+// in registers and stored in whole sectors; then, all together, those of its
+// tokens that no whole block has.  With kSpan = 1 a warp takes one token.
+
+// The codes of 16 rows, `have` a bit for each that is there; lane i makes row
+// i's exponent, which it returns, and scale (the whole warp doing each row's
+// would double the integer work, which is what fills the SM).
+template <typename T, int kRows>
+__device__ __forceinline__ int quantise_rows(const T* const (&x)[kRows], unsigned have, int lane,
+                                             uint32_t (&codes)[kRows]) {
+  Raw<T> v[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    v[i] = have >> i & 1 ? load4(x[i]) : Raw<T>{};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const uint32_t m = row_max(v[i]);
+    if (lane == i) top = m;
+  }
+  top = float_bits<T>(top);
+  if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const uint32_t m = finite_row_max(floats(v[i]));
+      if (lane == i) top = m;
+    }
+  }
+  const int e = q8_exponent(top);
+  const float scale = pow2f(-e);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) codes[i] = codes_of(floats(v[i]), __shfl_sync(0xffffffffu, scale, i));
+  return e;
+}
+
+// Bit i of the result: bits i .. i + 14 of x are set.
+__device__ __forceinline__ uint64_t fifteen(uint64_t x) {
+  x &= x >> 1;
+  x &= x >> 2;
+  x &= x >> 4;
+  return x & x >> 7;
+}
+
 template <typename T, int kSpan>
 __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 4 ? 5 : 7) write_kernel(const Q8WriteArgs a) {
-  static_assert(kSpan <= kBlock, "a run from the span's last place ends within 32 lanes");
   previous_done();
   next_may_begin();
   const int lane = threadIdx.x & 31;
@@ -123,57 +162,62 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 4 ? 5 : 7) writ
   if (item >= spans * a.Hkv * 2) return;
   const bool values = item & 1;
   const int h = static_cast<int>((item >> 1) % a.Hkv);
-  const int t0 = static_cast<int>((item >> 1) / a.Hkv) * kSpan;
-  // Lane i holds the slot of token t0 + i (the span and a run's rest behind
-  // it); past the last token nothing continues a run.
-  const int64_t slot = lane < a.T - t0 ? a.slots[static_cast<int64_t>(t0) + lane] : -1;
-  int64_t before = __shfl_up_sync(0xffffffffu, slot, 1);
-  if (lane == 0) before = t0 > 0 ? a.slots[t0 - 1] : -2;
-  const bool begins = slot >= 0 && (slot != before + 1 || before < 0 || (slot & (kBlock - 1)) == 0);
-  const bool ends = slot < 0 || begins;  // the run before ends here
-  const unsigned ending = __ballot_sync(0xffffffffu, ends);
-  unsigned todo = __ballot_sync(0xffffffffu, begins && lane < kSpan);
+  const int64_t t0 = (item >> 1) / a.Hkv * kSpan;
   const int64_t stride = values ? a.v_stride : a.k_stride;
-  const T* src = static_cast<const T*>(values ? a.v : a.k) + h * kHeadDim + lane * 4;
-  for (; todo; todo &= todo - 1) {
-    const int at = __ffs(todo) - 1;
-    const int64_t first = __shfl_sync(0xffffffffu, slot, at);
-    if (first >= a.num_slots) {
-      if (lane == 0) raise_error(a.err, kErrBadUnit);
-      continue;
+  const T* src = static_cast<const T*>(values ? a.v : a.k) + h * kHeadDim + lane * 4 + t0 * stride;
+  const int exps = kQ8ExpOffset + (values ? kBlock : 0);
+  auto slot_of = [&](int64_t t) { return t >= 0 && t < a.T ? a.slots[t] : -1; };
+  auto unit_of = [&](int64_t slot) {
+    return a.pages + ((slot >> 4) * a.Hkv + h) * static_cast<int64_t>(kQ8UnitBytes);
+  };
+  uint32_t codes[kSpan];
+  const T* x[kSpan];
+  // Lane i: the slot of token t0 + i of the span.
+  int64_t slot;
+  uint64_t whole = 0, mine = 1;  // whole blocks' first tokens; tokens of none (bit i: token t0 + i)
+  uint64_t follows = 0;          // tokens in the slot behind the token before
+  if constexpr (kSpan == 1) {
+    slot = slot_of(t0);
+  } else {
+    // Tokens t0 - 16 .. t0 + 31, bits 0 .. 47: which stand in the slot behind
+    // the token before, and which in a block's first.
+    const int64_t s0 = slot_of(t0 - 16 + lane), s1 = lane < 16 ? slot_of(t0 + 16 + lane) : -1;
+    int64_t p0 = __shfl_up_sync(0xffffffffu, s0, 1), p1 = __shfl_up_sync(0xffffffffu, s1, 1);
+    const int64_t last = __shfl_sync(0xffffffffu, s0, 31);
+    if (lane == 0) {
+      p0 = -1;  // of no consequence: no block that reaches the span began before
+      p1 = last;
     }
-    // at + 16 <= 31: the token after a whole block begins a run in some lane.
-    const int n = __ffs(ending >> (at + 1));
-    const int j0 = static_cast<int>(first & (kBlock - 1));
-    uint8_t* unit = a.pages + ((first >> 4) * a.Hkv + h) * static_cast<int64_t>(kQ8UnitBytes);
-    const T* x = src + static_cast<int64_t>(t0 + at) * stride;
-    uint32_t codes[kBlock];
-    int mine = 0;  // exponent of token `lane` of the run
-    if (n == kBlock) {
-      Raw<T> v[kBlock];
-#pragma unroll
-      for (int i = 0; i < kBlock; ++i) v[i] = load4(x + i * stride);
-      // Lane i makes row i's exponent and scale (the whole warp doing each
-      // row's would double the integer work, which is what fills the SM).
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < kBlock; ++i) {
-        const uint32_t m = row_max(v[i]);
-        if (lane == i) top = m;
+    auto bits = [](bool b0, bool b1) {
+      return static_cast<uint64_t>(__ballot_sync(0xffffffffu, b0)) |
+             static_cast<uint64_t>(__ballot_sync(0xffffffffu, b1)) << 32;
+    };
+    const uint64_t next = bits(p0 >= 0 && s0 == p0 + 1, p1 >= 0 && s1 == p1 + 1);
+    const uint64_t begins = bits(s0 >= 0 && (s0 & (kBlock - 1)) == 0, s1 >= 0 && (s1 & (kBlock - 1)) == 0);
+    const uint64_t there = bits(s0 >= 0, s1 >= 0);
+    const uint64_t first = begins & fifteen(next >> 1);
+    uint64_t member = first | first << 1;
+    member |= member << 2;
+    member |= member << 4;
+    member |= member << 8;
+    whole = first >> 16 & 0xffffu;
+    mine = (there & ~member) >> 16 & 0xffffu;
+    follows = next >> 16;
+    slot = __shfl_sync(0xffffffffu, s0, (lane + 16) & 31);  // of the span's tokens, lanes 0 .. 15
+  }
+
+  if constexpr (kSpan > 1) {
+    for (; whole; whole &= whole - 1) {
+      const int at = __ffsll(static_cast<long long>(whole)) - 1;
+      const int64_t begin = __shfl_sync(0xffffffffu, slot, at);
+      if (begin >= a.num_slots) {
+        if (lane == 0) raise_error(a.err, kErrBadUnit);
+        continue;
       }
-      top = float_bits<T>(top);
-      if (__any_sync(0xffffffffu, top >= 0x7f800000u)) {
 #pragma unroll
-        for (int i = 0; i < kBlock; ++i) {
-          const uint32_t m = finite_row_max(floats(v[i]));
-          if (lane == i) top = m;
-        }
-      }
-      mine = q8_exponent(top);
-      const float scale = pow2f(-mine);
-#pragma unroll
-      for (int i = 0; i < kBlock; ++i)
-        codes[i] = codes_of(floats(v[i]), __shfl_sync(0xffffffffu, scale, i));
+      for (int i = 0; i < kSpan; ++i) x[i] = src + (at + i) * stride;
+      const int e = quantise_rows(x, 0xffffu, lane, codes);
+      uint8_t* unit = unit_of(begin);
       if (values) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -191,26 +235,48 @@ __global__ void __launch_bounds__(kWriteWarps * 32, sizeof(T) == 4 ? 5 : 7) writ
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < kBlock; ++i)
+        for (int i = 0; i < kSpan; ++i)
           *reinterpret_cast<uint32_t*>(unit + q8_key_at(i, lane * 4)) = codes[i];
       }
-    } else {
-      for (int i = 0; i < n; ++i) {
-        const float4 f = floats(load4(x + i * stride));
-        const int e = q8_exponent(finite_row_max(f));
-        const uint32_t c = codes_of(f, pow2f(-e));
-        if (lane == i) mine = e;
-        if (values) {
+      if (lane < kBlock) unit[exps + lane] = static_cast<uint8_t>(e + 127);
+    }
+  }
+
+  // The other tokens.  Values: four of them in four slots that make a word go
+  // as words, the rest as bytes 16 apart (each a sector of its own, which is
+  // what such writes cost: 16384 scattered tokens 145 us, runs of 13 as bytes
+  // 111).
+  const bool in = lane < kSpan && (mine >> lane & 1) && slot >= 0;
+  if (in && slot >= a.num_slots) raise_error(a.err, kErrBadUnit);
+  const unsigned have = __ballot_sync(0xffffffffu, in && slot < a.num_slots);
+  if (have == 0) return;
 #pragma unroll
-          for (int d = 0; d < 4; ++d)
-            unit[q8_value_at(j0 + i, lane * 4 + d)] = static_cast<uint8_t>(c >> (8 * d));
-        } else {
-          *reinterpret_cast<uint32_t*>(unit + q8_key_at(j0 + i, lane * 4)) = c;
-        }
+  for (int i = 0; i < kSpan; ++i) x[i] = src + i * stride;
+  const int e = quantise_rows(x, have, lane, codes);
+  const unsigned on = have & static_cast<unsigned>(follows);
+  const unsigned quads = __ballot_sync(0xffffffffu, (slot & 3) == 0) & have & on >> 1 & on >> 2 & on >> 3;
+  unsigned bytes = have & ~(quads | quads << 1 | quads << 2 | quads << 3);
+#pragma unroll
+  for (int i = 0; i < kSpan; ++i) {
+    if (!(have >> i & 1)) continue;
+    const int64_t to = __shfl_sync(0xffffffffu, slot, i);
+    const int j = static_cast<int>(to & (kBlock - 1));
+    uint8_t* unit = unit_of(to);
+    if (!values) {
+      *reinterpret_cast<uint32_t*>(unit + q8_key_at(j, lane * 4)) = codes[i];
+    } else if (bytes >> i & 1) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) unit[q8_value_at(j, lane * 4 + d)] = static_cast<uint8_t>(codes[i] >> (8 * d));
+    } else if constexpr (kSpan > 3) {
+      if (i + 3 < kSpan && (quads >> i & 1)) {
+        uint32_t w[4] = {codes[i], codes[(i + 1) % kSpan], codes[(i + 2) % kSpan], codes[(i + 3) % kSpan]};
+        transpose4(w);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) *reinterpret_cast<uint32_t*>(unit + q8_value_at(j, lane * 4 + d)) = w[d];
       }
     }
-    if (lane < n) unit[kQ8ExpOffset + (values ? kBlock : 0) + j0 + lane] = static_cast<uint8_t>(mine + 127);
   }
+  if (have >> lane & 1) unit_of(slot)[exps + (slot & (kBlock - 1))] = static_cast<uint8_t>(e + 127);
 }
 
 // Two codes times a power of two, as two values of the output's type.

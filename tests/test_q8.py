@@ -75,6 +75,55 @@ def test_write(dev, dtype, T, Hkv, mode):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF, FP])
+@pytest.mark.parametrize("seed", range(6))
+def test_write_mixed_runs(dev, dtype, seed):
+    """Runs of any length from anywhere in a block, single tokens, whole blocks across the places
+    where a warp's tokens end, holes, and slots past the pool: 700 and more tokens of 8 heads."""
+    g = gen(100 + seed)
+    r = lambda n: int(torch.randint(0, n, (1,), generator=g))  # noqa: E731
+    P, at, slots = 260, 0, []
+    while len(slots) < 700 + seed:
+        at += r(20)                                   # where the next run begins
+        n = [1, 1 + r(5), 16, 15, 17, 1 + r(60), 16 * (1 + r(4))][r(7)]
+        if r(3) == 0:
+            at = -(-at // 16) * 16
+        slots += range(at, at + n)
+        at += n
+        if r(4) == 0:
+            slots += [-1] * (1 + r(3))
+    order = list(range(len(slots)))
+    if seed % 2:                                      # whole runs in another order
+        cut = sorted(r(len(slots)) for _ in range(6))
+        parts = [order[a:b] for a, b in zip([0] + cut, cut + [len(order)])]
+        order = [i for k in torch.randperm(len(parts), generator=g).tolist() for i in parts[k]]
+    slots = torch.tensor([slots[i] for i in order])
+    slots = torch.where(slots >= P * 16, torch.full_like(slots, -1), slots)
+    T, H = len(slots), 8
+    c = cache_of(P, 1, H, H)
+    old = torch.randint(0, 256, c.pages.shape, generator=g, dtype=torch.uint8)
+    c.pages.copy_(old)
+    x = (torch.randn(T, H, 128, generator=g) * torch.exp2(3 * torch.randn(T, H, 1, generator=g))).to(dtype)
+    if seed == 2:                                     # values that do not set a scale
+        x[::7, :, 3], x[::11, ::2, 9] = float("inf"), float("nan")
+    y = x.flip(0).contiguous()
+    want = old.numpy().copy()
+    free = Q.write(want, x, y, slots)
+    c.oasis_q8_write(x.cuda(), y.cuda(), slots.cuda())
+    assert c.oasis_q8_sync() == 0
+    got = c.pages.cpu().numpy()
+    assert np.array_equal(got[~free], want[~free]) and (got[free] & 127 == 127).all()
+    if seed == 0:                                     # the last run past the pool: a bit, the rest written
+        slots[-40:] = torch.arange(40) + P * 16 - 8
+        c.pages.copy_(old)
+        want = old.numpy().copy()
+        Q.write(want, x, y, slots)
+        c.oasis_q8_write(x.cuda(), y.cuda(), slots.cuda())
+        with pytest.raises(ob.OasisError):
+            c.oasis_q8_sync()
+        assert np.array_equal(c.pages.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
 def test_write_special_values(dev, dtype):
     rows = [[0.0], [-0.0], [float("inf")], [float("-inf"), 2.0], [float("nan"), -3.0],
             [float("nan"), float("inf"), 448.0], [torch.finfo(dtype).max], [torch.finfo(dtype).tiny],
