@@ -369,7 +369,7 @@ cudaError_t launch_write(const Q8WriteArgs& a, cudaStream_t s) {
   // us with one and sixteen: 128 scattered tokens 2.9, 5.6, a run of them 3.4,
   // 2.4; 256 3.8, 6.1 and 4.4, 2.3; 600 6.5, 6.6 and 7.1, 2.9.
   const int64_t rows = static_cast<int64_t>(a.T) * a.Hkv * 2;
-    const bool one = rows < 152 * 32;
+  const bool one = rows < 152 * 32;
   const int64_t items = one ? rows : (static_cast<int64_t>(a.T) + kLongSpan - 1) / kLongSpan * a.Hkv * 2;
   const unsigned grid = static_cast<unsigned>((items + kWriteWarps - 1) / kWriteWarps);
   return launch_early(one ? write_kernel<T, 1> : write_kernel<T, kLongSpan>, grid, kWriteWarps * 32, 0, s, 0, a);
