@@ -723,6 +723,66 @@ def test_calls_in_a_row_see_what_the_ones_before_wrote(dev):
     assert float(want[0].abs().sum()) > 0
 
 
+def test_calls_captured_on_two_streams_that_fork_and_join(dev):
+    """One graph whose work forks to a second stream and joins again, replayed: the same bytes as
+    the calls one by one."""
+    g = gen(34)
+    c = cache_of(30, 10, 8, 2)
+    fill(c, g)
+    lens = [100, 37, 0, 64]
+    table = Q.table_of(lens, 30, 10, g).cuda()
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    slots = torch.stack([Q.slots_of(table.cpu(), r, m - 1, m)[0] for r, m in enumerate(lens) if m]).cuda()
+    kv, _ = prefix_of(g, 2, 9, 140)
+    q, k, v = (torch.zeros(*s, dtype=BF, device=dev) for s in [(2, 4, 8, 128), (3, 2, 128), (3, 2, 128)])
+    o = [torch.zeros_like(q) for _ in range(4)]
+    back = torch.zeros(4, 2, 10, 2, 16, 128, dtype=BF, device=dev)
+    ws = [c.prefix_workspace(4, 2, 140) for _ in range(2)]
+    p = torch.softmax(torch.randn(4, 3, 700, generator=g), -1).cuda()
+    d = torch.softmax(torch.randn(4, 2, 700, generator=g), -1).cuda()
+    x = torch.randint(0, 700, (4, 2), generator=g).int().cuda()
+    ua, us = torch.rand(4, 2, generator=g).cuda(), torch.rand(4, generator=g).cuda()
+    tok, acc = torch.zeros(4, 3, dtype=torch.int32, device=dev), torch.zeros(4, dtype=torch.int32, device=dev)
+    side = torch.cuda.Stream()
+
+    def work(fork):
+        main = torch.cuda.current_stream()
+        c.oasis_q8_write(k, v, slots)
+        if fork:
+            side.wait_stream(main)
+        with torch.cuda.stream(side if fork else main):
+            c.oasis_q8_attn(q, table, n, o[0], causal=True)
+            c.oasis_prefix_attn(q, kv, 140, table, n, o[1], ws[0])
+            ob.oasis_verify_drafts(p, d, x, ua, us, tok, acc)
+        c.oasis_prefix_attn(q, kv, 140, table, n, o[2], ws[1], causal=True)
+        c.oasis_q8_read(table, n, back)
+        if fork:
+            main.wait_stream(side)
+        c.oasis_q8_attn(o[1], table, n, o[3])
+
+    outs = [*o, back, tok, acc]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work(True)
+    for i in range(4):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g))
+        us.copy_(torch.rand(4, generator=g))
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs]
+        for t in outs:
+            t.zero_()
+        work(False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, outs))
+        assert all(float(t.float().abs().sum()) > 0 for t in outs)
+    assert c.oasis_q8_sync() == 0
+
+
 def test_two_prefix_calls_at_once_with_scratch_of_their_own(dev):
     g = gen(32)
     c = cache_of(30, 10, 8, 2)
