@@ -620,7 +620,8 @@ OASIS_API int oasis_profile_read(oasis_ctx* ctx, double* ms_sum4,
  *          slots are skipped.
  * The write, read, attention and verification calls are asynchronous on the
  * caller's stream: none allocates, synchronises or leaves the current device
- * changed, and each may be captured into a graph.  A handle's calls may run
+ * changed, and each may be captured into a graph.  (Their kernels may start
+ * before the stream's earlier work has ended, and then wait for it.)  A handle's calls may run
  * on several streams at once as long as none writes pages another one reads
  * (and, for the prefix, each has scratch of its own); one host thread at a
  * time.  A bad page, slot or length does not fault: it raises a device error
@@ -728,10 +729,12 @@ OASIS_API int oasis_prefix_attn(oasis_q8* q8, int num_requests, int num_queries,
  *   w_0 + .. + w_j > u_sample[r] * (w_0 + .. + w_(V-1)),
  * w = max(p_k - q_k, 0), or p_k where that leaves nothing, or p_(n_r) when
  * all were accepted (k = n_r).  out_tokens[r] holds the k accepted drafts,
- * that token, then -1; n_accept[r] = k.  Sums are held to about 48 bits.  A
- * row without a positive entry (or with an infinite one) gives token -1; NaN
- * counts as 0; a draft outside [0, V) gives n_accept[r] = -1 and tokens -1
- * for its request.  Rows need not add up to one. */
+ * that token, then -1; n_accept[r] = k.  Sums are held to about 48 bits.
+ * Negative entries and NaN count as 0, for acceptance too.  A row without a
+ * positive entry gives token -1, as do infinite entries of the rows drawn
+ * from (p_k's or q_k's) and sums past fp32's range.  A draft outside [0, V)
+ * gives n_accept[r] = -1 and tokens -1 for its request.  Rows need not add up
+ * to one. */
 typedef struct {
   int32_t num_requests;   /* R >= 0 */
   int32_t num_drafts;     /* n, 0..64 */

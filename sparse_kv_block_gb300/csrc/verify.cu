@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     if (x < 0 || x >= V) {
       bad_s = 1;
     } else {
-      const float p = to_f(target[i * a.target_stride + x]);
-      const float q = draft ? to_f(draft[i * a.draft_stride + x]) : 1.f;
+      const float p = fmaxf(to_f(target[i * a.target_stride + x]), 0.f);
+      const float q = draft ? fmaxf(to_f(draft[i * a.draft_stride + x]), 0.f) : 1.f;
       if (!(static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(p))) atomicMin(&first_s, i);
     }
   }
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
         if (lane >= off) incl += o;
       }
       const double total = __shfl_sync(0xffffffffu, incl, 31);
-      int seg = -1;
+      int seg = total == 0.0 ? -1 : -2;  // nothing there; no sum
       double rest_of = 0.0;
       if (total > 0.0 && total < INFINITY) {
         const double threshold = static_cast<double>(a.u_sample[r]) * total;
@@ -260,13 +260,13 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
     const int seg = seg_s;
     if (seg < 0) {
       // Nothing is left of the difference: draw from p itself.
-      if (pass == 0 && (rows.q || rows.certain >= 0)) {
+      if (seg == -1 && pass == 0 && (rows.q || rows.certain >= 0)) {
         rows.q = nullptr;
         rows.certain = -1;
         __syncthreads();  // seg_s is written again
         continue;
       }
-      if (rank == 0 && tid == 0) out[k] = -1;  // no entry above zero
+      if (rank == 0 && tid == 0) out[k] = -1;  // no entry above zero, or an infinite one
       return;
     }
     if (seg % stride / kVerifyWarps != rank) return;

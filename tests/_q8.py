@@ -167,21 +167,23 @@ def verify(target, draft, x, ua, us, n_drafts=None):
             acc[r] = -1
             continue
         k = 0
-        while k < m and ua[r, k] * (q[r, k, x[r, k]] if q is not None else 1.0) < p[r, k, x[r, k]]:
+        positive = lambda a: np.where(a > 0, a, 0.0)  # noqa: E731  (NaN and negative entries count as 0)
+        while k < m and ua[r, k] * (positive(q[r, k, x[r, k]]) if q is not None else 1.0) < positive(p[r, k, x[r, k]]):
             out[r, k] = x[r, k]
             k += 1
         acc[r] = k
         w = p[r, k]
         if k < m:
             d = q[r, k] if q is not None else (np.arange(V) == x[r, k]) * max(1.0, p[r, k, x[r, k]])
-            left = np.maximum(np.where(w > 0, w, 0.0) - np.where(d > 0, d, 0.0), 0.0)  # NaN counts as 0
-            if left.sum() > 0:
+            if np.isposinf(d).any():
+                continue
+            left = np.maximum(positive(w) - positive(d), 0.0)
+            if left.sum() > 0 or np.isposinf(w).any():
                 w = left
-        w = np.where(w > 0, w, 0.0)
-        c = np.cumsum(w)
+        c = np.cumsum(positive(w))
         if c[-1] > 0 and np.isfinite(c[-1]):
             j = int(np.searchsorted(c, us[r] * c[-1], side="right"))
-            out[r, k] = min(j, int(np.nonzero(w)[0][-1]))
+            out[r, k] = min(j, int(np.nonzero(positive(w))[0][-1]))
     return out, acc
 
 

@@ -104,6 +104,34 @@ def test_equal_distributions_and_empty_rows(dev):
     assert np.array_equal(acc, wa) and np.array_equal(tok, wt) and tok[1, 0] == -1
 
 
+def test_nan_negative_and_infinite_entries(dev):
+    """NaN and negative entries count as 0, for acceptance too; an infinite entry of a row that is
+    drawn from, p's or the one subtracted, leaves no token."""
+    p, q, x, ua, us = draw(9, 2, 1500, gen(9))
+    ua[:, 0], ua[:, 1] = 0.0, 0.5
+    nan, inf = float("nan"), float("inf")
+    at = lambda r, i: (r, i, int(x[r, i]))  # noqa: E731
+    q[at(0, 0)] = nan                                  # 0 < p: accepted
+    p[at(1, 0)] = nan                                  # refused
+    q[at(2, 0)], p[at(2, 0)], ua[2, 0] = -0.5, 0.0, 0.5    # 0 < 0: refused
+    p[at(3, 0)] = -1.0                                 # refused, and no part of the difference
+    p[at(4, 0)], q[4, 0, 7] = 0.0, inf                 # refused, no difference
+    p[at(5, 0)], p[5, 0, 7] = 0.0, inf
+    q[at(6, 0)] = q[at(6, 1)] = 0.0                    # both accepted, p drawn from
+    p[6, 2, 1200] = inf
+    q[7, 0, :] = -q[7, 0, :]                           # accepted; the second as it comes
+    p[8], q[8, 0, 3] = -p[8], inf
+    for dtype in (FP, BF, HF):
+        pt, qt = p.to(dtype), q.to(dtype)
+        for d in (qt, None):
+            wt, wa = Q.verify(pt, d, x, ua, us)
+            tok, acc = go(pt, d, x, ua, us)
+            assert np.array_equal(acc, wa) and np.array_equal(tok, wt)
+            if d is not None:
+                assert acc[0] >= 1 and acc[7] >= 1 and (acc[1:6] == 0).all() and acc[6] == 2 and acc[8] == 0
+                assert (tok[[4, 5, 8], 0] == -1).all() and tok[6, 2] == -1 and (tok[[1, 2, 3], 0] >= 0).all()
+
+
 @pytest.mark.parametrize("V", [1, 33, 2049, 40000])
 def test_borders(dev, V):
     """u on the exact borders of dyadic probabilities: the first sum above u * total wins; u = 0
