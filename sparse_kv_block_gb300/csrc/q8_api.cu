@@ -2,6 +2,7 @@
 // argument checks, the handle and the launches.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -103,7 +104,8 @@ OASIS_API int oasis_q8_init(const oasis_q8_config* cfg, void* pages, void* works
     return OASIS_ECUDA;
   // The caller's memory may still be written by what it was used for before.
   if (cudaDeviceSynchronize() != cudaSuccess) return OASIS_ECUDA;
-  if (cudaMemset(workspace, 0, 256) != cudaSuccess) return OASIS_ECUDA;
+  // (A memset may return early; the caller's streams need not wait for it.)
+  if (cudaMemset(workspace, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return OASIS_ECUDA;
   oasis_q8* q = new (std::nothrow) oasis_q8;
   if (!q) return OASIS_ENOMEM;
   q->cfg = *cfg;
@@ -137,6 +139,8 @@ OASIS_API int oasis_q8_sync(oasis_q8* q8, uint32_t* device_bits) {
   if (device_bits) *device_bits = bits;
   if (!bits) return OASIS_OK;
   if (int rc = q8->cuda(cudaMemset(q8->err, 0, sizeof bits), "clear device error word")) return rc;
+  // A later call's bits on a stream of the caller's must come after it.
+  if (int rc = q8->cuda(cudaDeviceSynchronize(), "cudaDeviceSynchronize")) return rc;
   return q8->fail(OASIS_EDEVICE, "device error bits 0x%x", bits);
 }
 
@@ -391,9 +395,13 @@ OASIS_API int oasis_verify_drafts(const oasis_verify_args* a, void* stream) {
   v.n = a->num_drafts;
   v.V = a->vocab;
   v.type = a->type;
-  // Load the kernels on their first use of the process, so that this may be
-  // inside a stream capture.
-  static const cudaError_t loaded = preload_verify_kernels();
-  if (loaded != cudaSuccess) return OASIS_ECUDA;
+  // Load the kernels on a device's first call, so that it may be inside a
+  // stream capture.
+  static std::atomic<uint64_t> loaded{0};
+  const uint64_t bit = a->device < 64 ? 1ull << a->device : 0;
+  if (!(loaded.load(std::memory_order_acquire) & bit)) {
+    if (preload_verify_kernels() != cudaSuccess) return OASIS_ECUDA;
+    loaded.fetch_or(bit, std::memory_order_release);
+  }
   return launch_verify(v, static_cast<cudaStream_t>(stream)) == cudaSuccess ? OASIS_OK : OASIS_ECUDA;
 }
