@@ -4,9 +4,10 @@
 //
 // One CTA, or one cluster of CTAs where there are few (request, KV head)
 // pairs, per pair; every warp takes groups of 64 tokens (four units) through
-// a ring of its own, one bulk copy per unit.  The two products run on
-// mma.sync m16n8k16 with tokens, then dims, as M and up to 16 query columns
-// (query s, head gi: column s * G + gi) as N.  Codes become fp16 exactly;
+// a ring of its own, two bulk copies per unit (its keys; its values and
+// exponents).  The two products run on mma.sync m16n8k16 with tokens, then
+// dims, as M and up to 16 query columns (query s, head gi: column s * G + gi)
+// as N.  Codes become fp16 exactly;
 // which token stands for which matrix row is chosen so that a lane's 16-byte
 // loads are whole fragments and the transposed weights (movmatrix) meet the
 // value codes as they lie:
