@@ -621,12 +621,12 @@ OASIS_API int oasis_profile_read(oasis_ctx* ctx, double* ms_sum4,
  * The write, read, attention and verification calls are asynchronous on the
  * caller's stream: none allocates, synchronises or leaves the current device
  * changed, and each may be captured into a graph.  (Their kernels may start
- * before the stream's earlier work has ended, and then wait for it.)  A handle's calls may run
- * on several streams at once as long as none writes pages another one reads
- * (and, for the prefix, each has scratch of its own); one host thread at a
- * time.  A bad page, slot or length does not fault: it raises a device error
- * bit (BAD_BLOCK_ID for a table entry or a length, BAD_UNIT for a slot), read
- * by oasis_q8_sync, and the block or token is left out.
+ * before the stream's earlier work has ended, and then wait for it.)  A
+ * handle's calls may run on several streams at once as long as none writes
+ * pages another one reads (and each that takes scratch has its own); one host
+ * thread at a time.  A bad page, slot or length does not fault: it raises a
+ * device error bit (BAD_BLOCK_ID for a table entry or a length, BAD_UNIT for a
+ * slot), read by oasis_q8_sync, and the block or token is left out.
  * ------------------------------------------------------------------------ */
 #define OASIS_BF16 0
 #define OASIS_FP16 1
@@ -702,7 +702,15 @@ OASIS_API int oasis_q8_read(oasis_q8* q8, int num_requests, const int32_t* page_
  * and S * R * Hq < 2^31. */
 OASIS_API int oasis_q8_attn(oasis_q8* q8, int num_requests, int num_queries, int causal,
                             const void* q, int type, const int32_t* page_table,
-                            const int32_t* seq_len, void* out, void* stream);
+                            const int32_t* seq_len, void* out, void* workspace,
+                            size_t workspace_bytes, void* stream);
+/* Scratch with which oasis_q8_attn of these sizes can cut requests into parts
+ * by their lengths (device memory, 256-byte aligned; 0: it would not).  With
+ * a NULL workspace it works without, slower for batches of unequal lengths.
+ * A call's scratch must not be given to another that may run at the same
+ * time. */
+OASIS_API int oasis_q8_attn_workspace(const oasis_q8* q8, int num_requests, int num_queries,
+                                      size_t* bytes);
 
 /* Scratch that oasis_prefix_attn wants for these sizes (device memory,
  * 256-byte aligned; 0 is possible).  A call's scratch must not be given to

@@ -417,9 +417,7 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
   if (warp == kTiles * 4 + 1) tmem_free(tmem, Lay::kColumns);
 }
 
-// The shares' rows joined: a warp a row, each lane a share's maximum and sum,
-// then four dims of every share.  (Plain loads: the launches that write them
-// may have run beside this one's beginning.)
+// The shares' rows joined: a warp a row.
 template <typename T>
 __global__ void __launch_bounds__(128) join_kernel(const PrefixArgs a) {
   const int lane = threadIdx.x & 31;
@@ -434,39 +432,9 @@ __global__ void __launch_bounds__(128) join_kernel(const PrefixArgs a) {
            ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + c - s * a.G) * kHeadDim + lane * 4;
   previous_done();
   next_may_begin();
-  const int shares = a.splits + 1;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float m = -INFINITY, sum = 0.f;
-  for (int i0 = 0; i0 < shares; i0 += 32) {
-    const int some = min(shares - i0, 32);
-    constexpr int kBatch = 8;
-    const float2 st = lane < some ? __ldcg(a.stat + (i0 + lane) * rows + row) : make_float2(-INFINITY, 0.f);
-    const float4* part = reinterpret_cast<const float4*>(a.part) + (i0 * rows + row) * 32 + lane;
-    float4 x[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) x[b] = __ldcg(part + min(b, some - 1) * rows * 32);
-    float top = st.x;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    top = fmaxf(top, m);
-    const float old = scale_of(m, top), w = scale_of(st.x, top);
-    float l = w * st.y;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    sum = fmaf(sum, old, l);
-    scale4(acc, old);
-    m = top;
-    for (int i = 0; i < some; i += kBatch) {
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const float f = __shfl_sync(0xffffffffu, w, (i + b) & 31);
-        if (i + b < some) add4(acc, f, x[b]);
-      }
-      if (i + kBatch < some)
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) x[b] = __ldcg(part + min(i + kBatch + b, some - 1) * rows * 32);
-    }
-  }
+  float sum;
+  const float4 acc = join_shares(reinterpret_cast<const float4*>(a.part) + row * 32, a.stat + row, rows,
+                                 a.splits + 1, lane, sum);
   store4(out, make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum));
 }
 

@@ -108,6 +108,46 @@ __device__ __forceinline__ void add4(float4& a, float f, const float4& x) {
   a.z = fmaf(f, x.z, a.z);
   a.w = fmaf(f, x.w, a.w);
 }
+// A warp joins a row's shares, `stride` rows apart: each lane a share's maximum
+// and sum, then four dims of every share.  (Loads past L1: the launches that
+// write them may have run beside this one's beginning.)
+__device__ __forceinline__ float4 join_shares(const float4* part, const float2* stat, int64_t stride, int shares,
+                                              int lane, float& sum) {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY;
+  sum = 0.f;
+  for (int i0 = 0; i0 < shares; i0 += 32) {
+    const int some = min(shares - i0, 32);
+    constexpr int kBatch = 8;
+    const float2 st = lane < some ? __ldcg(stat + (i0 + lane) * stride) : make_float2(-INFINITY, 0.f);
+    const float4* from = part + i0 * stride * 32 + lane;
+    float4 x[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) x[b] = __ldcg(from + min(b, some - 1) * stride * 32);
+    float top = st.x;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    top = fmaxf(top, m);
+    const float old = scale_of(m, top), w = scale_of(st.x, top);
+    float l = w * st.y;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    sum = fmaf(sum, old, l);
+    scale4(acc, old);
+    m = top;
+    for (int i = 0; i < some; i += kBatch) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float f = __shfl_sync(0xffffffffu, w, (i + b) & 31);
+        if (i + b < some) add4(acc, f, x[b]);
+      }
+      if (i + kBatch < some)
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) x[b] = __ldcg(from + min(i + kBatch + b, some - 1) * stride * 32);
+    }
+  }
+  return acc;
+}
 __device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));

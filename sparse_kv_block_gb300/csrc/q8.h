@@ -49,6 +49,17 @@ struct Q8AttnArgs {
   // r) * S * G + s * G + gi [d] in units of 2^m, and (m, sum).
   float* part;
   float2* stat;
+  // Set too: requests are cut into parts by their lengths.  Row (CTA * S * G +
+  // s * G + gi) of the above; plan[r]: the parts before request r's.
+  int* plan;                 // [R + 1]
+  int columns, warps;        // of Q8Split
+};
+
+// Parts of a batch's requests, of about one length, and their scratch.
+struct Q8Split {
+  int columns;               // parts over all requests, at most (a CTA each and KV head); 0: not cut
+  int warps;                 // of a CTA
+  size_t part_bytes, stat_bytes, bytes;
 };
 
 // Shares and row tiles of the prefix attention, and its scratch.
@@ -112,6 +123,7 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size
 cudaError_t launch_q8_write(const Q8WriteArgs& a, cudaStream_t s);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
 cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s);
+Q8Split q8_split(int R, int S, int G, int Hkv, int max_blocks);
 PrefixShape prefix_shape(int R, int S, int G, int Hkv, int prefix_len);
 // The map covers the prefix [Hkv][blocks][2][B][d] with boxes of 8 blocks'
 // keys or values, 64 dims.

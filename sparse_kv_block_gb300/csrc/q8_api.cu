@@ -277,15 +277,38 @@ int prefix_map(oasis_q8* q8, const void* kv, int blocks, CUtensorMap* map) {
 
 }  // namespace
 
+OASIS_API int oasis_q8_attn_workspace(const oasis_q8* q8, int num_requests, int num_queries, size_t* bytes) {
+  if (!q8 || !bytes || num_requests < 0 || num_requests > 65535 || num_queries < 1 || num_queries > kQ8MaxQueries)
+    return OASIS_EINVAL;
+  *bytes = q8_split(num_requests, num_queries, q8->G, q8->cfg.num_kv_heads, q8->cfg.max_blocks).bytes;
+  return OASIS_OK;
+}
+
 OASIS_API int oasis_q8_attn(oasis_q8* q8, int num_requests, int num_queries, int causal,
                             const void* q, int type, const int32_t* page_table,
-                            const int32_t* seq_len, void* out, void* stream) {
+                            const int32_t* seq_len, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream) {
   if (!q8) return OASIS_EINVAL;
   Q8AttnArgs a{};
   if (int rc = attn_args(q8, "q8_attn", num_requests, num_queries, causal, q, type, page_table,
                          seq_len, out, &a))
     return rc;
+  if (workspace && !aligned(workspace, 256))
+    return q8->fail(OASIS_EINVAL, "q8_attn: workspace not 256-byte aligned");
   if (num_requests == 0) return OASIS_OK;
+  if (workspace) {
+    const Q8Split sp = q8_split(num_requests, num_queries, q8->G, q8->cfg.num_kv_heads, q8->cfg.max_blocks);
+    if (workspace_bytes < sp.bytes)
+      return q8->fail(OASIS_EINVAL, "q8_attn: workspace under %zu bytes", sp.bytes);
+    if (sp.columns) {
+      uint8_t* ws = static_cast<uint8_t*>(workspace);
+      a.part = reinterpret_cast<float*>(ws);
+      a.stat = reinterpret_cast<float2*>(ws + sp.part_bytes);
+      a.plan = reinterpret_cast<int*>(ws + sp.part_bytes + sp.stat_bytes);
+      a.columns = sp.columns;
+      a.warps = sp.warps;
+    }
+  }
   OnDevice dev(q8->cfg.device);
   if (int rc = q8->cuda(dev.error(), "cudaSetDevice")) return rc;
   return q8->cuda(launch_q8_attn(a, static_cast<cudaStream_t>(stream)), "q8_attn launch");

@@ -3,7 +3,8 @@
 // queries of that head).
 //
 // One CTA, or one cluster of CTAs where there are few (request, KV head)
-// pairs, per pair; every warp takes groups of 64 tokens (four units) through
+// pairs, per pair; or, given scratch, as many CTAs a request as its length
+// asks for, joined by a second launch.  Every warp takes groups of 64 tokens (four units) through
 // a ring of its own, two bulk copies per unit (its keys; its values and
 // exponents).  The two products run on mma.sync m16n8k16 with tokens, then
 // dims, as M and up to 16 query columns (query s, head gi: column s * G + gi)
@@ -29,6 +30,9 @@
 #include "q8.cuh"
 #include "q8.h"
 
+#ifndef NOSPLIT
+#define NOSPLIT 0
+#endif
 namespace oasis {
 namespace {
 
@@ -36,6 +40,8 @@ constexpr int kGroupUnits = 4;
 constexpr int kGroupTokens = kGroupUnits * kBlock;           // 64
 constexpr int kGroupBytes = kGroupUnits * kQ8UnitBytes;      // 16512
 constexpr float kWeightLog2 = 14.f;
+constexpr int kSplitRequests = 128;  // requests of a batch that can be cut into parts
+constexpr int kLeastGroups = 4;      // of a part's warp
 
 template <int W, int kNT>
 struct Layout {
@@ -73,6 +79,64 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) 
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 
+// Which part of which request a CTA of column `col` takes.  A part is up to W *
+// m groups, m the least number with which no more than a.columns parts come
+// out; every warp finds it from all lengths (up to 128, four a lane).
+template <int W>
+__device__ __forceinline__ bool part_of(const Q8AttnArgs& a, int col, int warp, int lane, int& r, int& rank,
+                                        int& parts, int& len) {
+  int lens[kSplitRequests / 32], groups[kSplitRequests / 32];
+  int total = 0, longest = 0;
+#pragma unroll
+  for (int j = 0; j < kSplitRequests / 32; ++j)
+    lens[j] = j * 32 + lane < a.R ? __ldcg(a.len + j * 32 + lane) : 0;
+#pragma unroll
+  for (int j = 0; j < kSplitRequests / 32; ++j) {
+    groups[j] = (min(max(lens[j], 0), a.max_blocks * kBlock) + kGroupTokens - 1) / kGroupTokens;
+    total += groups[j];
+    longest = max(longest, groups[j]);
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  int lo = max((total + W * a.columns - 1) / (W * a.columns), kLeastGroups);
+  int hi = max((longest + W - 1) / W, lo);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < kSplitRequests / 32; ++j) n += (groups[j] + W * mid - 1) / (W * mid);
+    if (static_cast<int>(__reduce_add_sync(0xffffffffu, n)) <= a.columns) hi = mid;
+    else lo = mid + 1;
+  }
+  bool found = false;
+  int before = 0;
+#pragma unroll
+  for (int j = 0; j < kSplitRequests / 32; ++j) {
+    if (j * 32 >= a.R) break;
+    const int n = (groups[j] + W * lo - 1) / (W * lo);
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    const int from = before + incl - n;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0 && j * 32 + lane <= a.R) a.plan[j * 32 + lane] = from;
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    const unsigned here = __ballot_sync(0xffffffffu, col >= from && col < from + n);
+    if (here) {
+      const int src = __ffs(here) - 1;
+      found = true;
+      r = j * 32 + src;
+      rank = col - __shfl_sync(0xffffffffu, from, src);
+      parts = __shfl_sync(0xffffffffu, n, src);
+      len = __shfl_sync(0xffffffffu, lens[j], src);
+    }
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0 && lane == 0) a.plan[a.R] = before;
+  return found;
+}
+
 template <typename T, int W, int kNT>
 __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
     attn_kernel(const Q8AttnArgs a, int most, int each) {
@@ -82,13 +146,22 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
   // A prefix's share of pages needs nothing of the launch ahead, the prefix's
   // own, which has itself waited for what came before.  (This grid has not:
   // it reads past L1, which may hold what was there before.)
-  if (!a.part) previous_done();
+  const bool beside = a.part && !a.plan;
+  if (!beside) previous_done();
   next_may_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int pair = blockIdx.x / most;
-  const int rank = static_cast<int>(most == 1 ? 0u : cluster_rank());
-  const int r = pair / a.Hkv, h = pair - r * a.Hkv;
+  int r, h, rank, parts = 0, len;
+  if (a.plan) {
+    h = static_cast<int>(blockIdx.x % a.Hkv);
+    if (!part_of<W>(a, static_cast<int>(blockIdx.x / a.Hkv), warp, lane, r, rank, parts, len)) return;
+  } else {
+    const int pair = blockIdx.x / most;
+    rank = static_cast<int>(most == 1 ? 0u : cluster_rank());
+    r = pair / a.Hkv;
+    h = pair - r * a.Hkv;
+    len = __ldcg(a.len + r);
+  }
   const int col0 = blockIdx.y * kCols;                 // first column of this CTA
   const int cols = min(a.S * a.G - col0, kCols);
 
@@ -112,7 +185,6 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
     const int64_t b = (first + static_cast<int64_t>(k) * step) * kGroupUnits + lane;
     return lane < kGroupUnits && b < a.max_blocks ? __ldcg(row + b) : -1;
   };
-  int len = __ldcg(a.len + r);
   int page = page_of(0);
   uint4 qv[4];  // warp nt < kNT: of column 8 nt + g, dims 64 (j / 2) + 16 t + 8 (j % 2) .. + 7
   {
@@ -135,10 +207,11 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
   }
   const int groups = (len + kGroupTokens - 1) / kGroupTokens;
   // A request takes as many of the cluster's CTAs as have `each` groups a warp
-  // (one for a short one); the others leave at once.
-  const int cluster = min(most, max((groups + W * each - 1) / (W * each), 1));
+  // (one for a short one); the others leave at once, though their room is kept
+  // until the whole cluster has ended.
+  const int cluster = parts ? parts : min(most, max((groups + W * each - 1) / (W * each), 1));
   if (rank >= cluster) {
-    if (a.part && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) previous_done();  // see the end
+    if (beside && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) previous_done();  // see the end
     return;
   }
   step = cluster * W;
@@ -517,7 +590,8 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
       join_sum(msum, sum, pml[w * kCols + c], pl[w * kCols + c]);
     }
   };
-  if (cluster > 1) {
+  const int gang = parts ? 1 : cluster;  // CTAs that join here
+  if (gang > 1) {
     for (int c = warp; c < cols; c += W) {
       float mx = -INFINITY, msum = -INFINITY, sum = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -534,7 +608,7 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
   constexpr int kMine = (kCols + W - 1) / W;  // columns of a warp at most
   float4 acc[kMine];
   float sum[kMine], msum[kMine];
-  auto column = [&](int j) { return (j * cluster + rank) * W + warp; };
+  auto column = [&](int j) { return (j * gang + (gang > 1 ? rank : 0)) * W + warp; };
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     const int c = column(j);
@@ -543,11 +617,11 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
     msum[j] = -INFINITY;
     if (c >= cols) continue;
     float mx = -INFINITY;
-    if (cluster == 1) {
+    if (gang == 1) {
       of_warps(c, acc[j], mx, msum[j], sum[j]);
     } else {
-      for (int i = 0; i < cluster; ++i) mx = fmaxf(mx, load_remote(mm + c, i));
-      for (int i = 0; i < cluster; ++i) {
+      for (int i = 0; i < gang; ++i) mx = fmaxf(mx, load_remote(mm + c, i));
+      for (int i = 0; i < gang; ++i) {
         add4(acc[j], scale_of(load_remote(mm + c, i), mx), load_remote4(merged + c * kHeadDim + lane * 4, i));
         join_sum(msum[j], sum[j], load_remote(mml + c, i), load_remote(ml + c, i));
       }
@@ -560,7 +634,8 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
     const int c = column(j);
     if (c >= cols) continue;
     if (a.part) {  // a share among others, joined later
-      const int64_t at = (static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0 + c;
+      const int64_t at =
+          (parts ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(h) * a.R + r) * (a.S * a.G) + col0 + c;
       store4(a.part + at * kHeadDim + lane * 4, acc[j]);
       if (lane == 0) a.stat[at] = make_float2(msum[j], sum[j]);
       continue;
@@ -577,9 +652,9 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
   // Beside another launch that writes shares: who waits for this grid has to
   // have waited for that one.  One CTA does it for all (others would keep SMs
   // from the CTAs behind them).
-  if (a.part && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+  if (beside && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
     previous_done();
-  if (cluster == 1) return;
+  if (gang == 1) return;
   cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
 template <typename T, int W, int kNT>
@@ -637,10 +712,94 @@ cudaError_t launch_n(const Q8AttnArgs& a, cudaStream_t s) {
   return launch_t<T, 2, 2>(a, col_groups, s);
 }
 
+// The parts of each request joined: a warp a row of out.
+template <typename T>
+__global__ void __launch_bounds__(128) join_parts(const Q8AttnArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(a.S) * a.R * a.Hq) return;
+  const int hq = static_cast<int>(row % a.Hq), r = static_cast<int>(row / a.Hq % a.R);
+  const int s = static_cast<int>(row / a.Hq / a.R), h = hq / a.G;
+  const int cols = a.S * a.G, c = s * a.G + hq - h * a.G;
+  previous_done();
+  next_may_begin();
+  const int first = __ldcg(a.plan + r), parts = __ldcg(a.plan + r + 1) - first;
+  const int64_t at = (static_cast<int64_t>(first) * a.Hkv + h) * cols + c;  // of the first part
+  float sum;
+  const float4 acc = join_shares(reinterpret_cast<const float4*>(a.part) + at * 32, a.stat + at,
+                                 static_cast<int64_t>(a.Hkv) * cols, parts, lane, sum);
+  // What a query sees nothing of is 0.
+  const float4 v = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum);
+  if (a.out_fp32) store4(static_cast<float*>(a.out) + row * kHeadDim + lane * 4, v);
+  else store4(static_cast<T*>(a.out) + row * kHeadDim + lane * 4, v);
+}
+
+template <typename T, int W, int kNT>
+cudaError_t launch_split(const Q8AttnArgs& a, cudaStream_t s) {
+  const cudaError_t e =
+      launch_early(attn_kernel<T, W, kNT>,
+                   dim3(static_cast<unsigned>(a.columns) * a.Hkv, (a.S * a.G + 8 * kNT - 1) / (8 * kNT)), W * 32,
+                   Layout<W, kNT>::kBytes, s, 0, a, 1, 1);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(a.S) * a.R * a.Hq;
+  return launch_early(a.out_fp32 ? join_parts<float> : join_parts<T>, static_cast<unsigned>((rows + 3) / 4), 128, 0,
+                      s, 0, a);
+}
+
+template <typename T>
+cudaError_t launch_split(const Q8AttnArgs& a, int warps, cudaStream_t s) {
+  if (a.S * a.G <= 8) return launch_split<T, 4, 1>(a, s);
+  return warps == 2 ? launch_split<T, 2, 2>(a, s) : launch_split<T, 4, 2>(a, s);
+}
+
 }  // namespace
+
+// Cutting requests into parts costs some 5 us (the parts' sizes, a second
+// launch) and gains where lengths differ or pairs are few: one round of CTAs of
+// about one size fills the card, where a cluster ends at eight CTAs and keeps
+// the room of those that a short request leaves idle.  So: where the card holds
+// at least 1.7 CTAs a pair, and there are either 7000 groups of unequal
+// requests, or eight groups a warp fewer.  GB300, us without and with (8 KV
+// heads of four query heads, lengths uniform up to the given one; in brackets
+// four queries): 2 x 131072 118, 84 [157, 87]; 2 x 32000 34, 25 [46, 32];
+// 5 x 30000 32, 27 [38, 35.5]; 24 x 9001 51.5, 49.5 [74, 61]; 38 x 8192 [94, 80];
+// 20 x 3000 22, 20.5 [39, 28]; one of 131072 104, 57 [140, 59], of 32768 30, 22
+// [43, 26].  But 20 x 2000 18, 19; 8 x 4000 16, 18; and where rounds are needed
+// 100 x 4000 81, 83 [111, 121].
+Q8Split q8_split(int R, int S, int G, int Hkv, int max_blocks) {
+  Q8Split p{};
+  if (R < 1 || R > kSplitRequests) return p;
+  const int cols = S * G, col_groups = (cols + 15) / 16, CTAs = cols <= 8 ? 3 : 2;
+  const int64_t pairs = static_cast<int64_t>(R) * Hkv * col_groups;
+  const int64_t groups = (max_blocks + kGroupUnits - 1) / kGroupUnits;
+  // Two warps a CTA with two column tiles where parts of four would be a
+  // quarter of a pair or more: 24 x 9001 65, 61 us with four, two; 40 x 4000
+  // 64, 56; but 5 x 30000 35, 38, one of 131072 59, 66.
+  const bool fine = cols > 8 && pairs * 4 > 152 * CTAs;
+  p.warps = fine ? 2 : 4;
+  const int64_t slots = 152 * CTAs * (fine ? 2 : 1);
+  if (pairs * 17 > slots * 10) return p;
+  // Groups of a warp at the longest: in clusters (as launch_t takes them), in parts.
+  int64_t cluster = 1;
+  while (cluster < 8 && pairs * cluster * 2 <= 152 * CTAs) cluster *= 2;
+  const int64_t whole = groups / (cluster * 4);
+  const int64_t part = pairs * groups / (slots * p.warps);
+  const bool gains = (R > 1 && pairs * groups >= 7000) || whole >= (part > kLeastGroups ? part : kLeastGroups) + 8;
+  if (!gains) return p;
+  p.columns = static_cast<int>(slots / (static_cast<int64_t>(Hkv) * col_groups));
+  const int64_t rows = static_cast<int64_t>(p.columns) * Hkv * cols;
+  auto up = [](int64_t n) { return static_cast<size_t>((n + 255) / 256 * 256); };
+  p.part_bytes = up(rows * kHeadDim * 4);
+  p.stat_bytes = up(rows * 8);
+  p.bytes = p.part_bytes + p.stat_bytes + up((R + 1) * 4);
+  return p;
+}
 
 cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s) {
   if (a.R == 0) return cudaSuccess;
+  if (a.plan)
+    return a.type == kBf16 ? launch_split<__nv_bfloat16>(a, a.warps, s) : launch_split<__half>(a, a.warps, s);
   return a.type == kBf16 ? launch_n<__nv_bfloat16>(a, s) : launch_n<__half>(a, s);
 }
 
@@ -652,6 +811,9 @@ cudaError_t configure_all() {
   if (e == cudaSuccess) e = configure<T, 1, 1>();
   if (e == cudaSuccess) e = configure<T, 4, 2>();
   if (e == cudaSuccess) e = configure<T, 2, 2>();
+  cudaFuncAttributes at;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, join_parts<T>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, join_parts<float>);
   return e;
 }
 }  // namespace

@@ -151,7 +151,8 @@ EXPORTS = {
     "oasis_q8_set_wait_limit": (c_int, [_P, ctypes.c_longlong]),
     "oasis_q8_write": (c_int, [_P, _P, _P, c_int, c_int64, c_int64, _P, c_int, _P]),
     "oasis_q8_read": (c_int, [_P, c_int, _P, _P, _P, c_int, c_int, _P]),
-    "oasis_q8_attn": (c_int, [_P, c_int, c_int, c_int, _P, c_int, _P, _P, _P, _P]),
+    "oasis_q8_attn": (c_int, [_P, c_int, c_int, c_int, _P, c_int, _P, _P, _P, _P, c_size_t, _P]),
+    "oasis_q8_attn_workspace": (c_int, [_P, c_int, c_int, POINTER(c_size_t)]),
     "oasis_prefix_workspace": (c_int, [_P, c_int, c_int, c_int, POINTER(c_size_t)]),
     "oasis_prefix_attn": (c_int, [_P, c_int, c_int, c_int, _P, c_int, _P, c_int, c_int, _P, _P,
                                   _P, _P, c_size_t, _P]),
@@ -615,6 +616,7 @@ class Q8Cache:
         self._lib, self._dev = lib(), int(cfg.device)
         self._Hq, self._Hkv, self._max_blocks = int(cfg.num_q_heads), int(cfg.num_kv_heads), int(cfg.max_blocks)
         self._out_fp32 = bool(cfg.out_fp32)
+        self._scratch = {}  # bytes that attention over (R, S) can use
 
     def _check(self, rc: int) -> None:
         if rc != OASIS_OK:
@@ -691,12 +693,38 @@ class Q8Cache:
         return (S, _want("q", q, dt, shape, self._dev), _TYPES[dt],
                 _want("out", out, torch.float32 if self._out_fp32 else dt, shape, self._dev))
 
-    def oasis_q8_attn(self, q, page_table, seq_len, out, causal=False, stream=None) -> None:
-        """q, out [S][R][Hq][128]."""
+    def oasis_q8_attn_workspace(self, R: int, S: int) -> int:
+        n = c_size_t(0)
+        rc = lib().oasis_q8_attn_workspace(self.q8, R, S, ctypes.byref(n))
+        if rc != OASIS_OK:
+            raise OasisError(rc, "q8_attn_workspace: bad size")
+        return n.value
+
+    def oasis_q8_attn(self, q, page_table, seq_len, out, causal=False, stream=None, workspace=None) -> None:
+        """q, out [S][R][Hq][128].  workspace: scratch of oasis_q8_attn_workspace bytes (uint8),
+        by default taken from the allocator for this call (on its stream, so that it is also right
+        inside a graph's capture)."""
         R, table, lens = self._table(page_table, seq_len)
         S, qp, typ, o = self._queries(q, out, R)
-        self._check(self._lib.oasis_q8_attn(self.q8, R, S, 1 if causal else 0, qp, typ, table, lens, o,
-                                            _stream_on(stream, self._dev)))
+        st = _stream_on(stream, self._dev)
+        if workspace is None:
+            n = self._scratch.get((R, S))
+            if n is None:
+                n = self._scratch[R, S] = self.oasis_q8_attn_workspace(R, S) if 1 <= S <= 4 else 0
+            if n:
+                workspace = self._scratch_on(n, stream)
+        else:
+            n = workspace.numel()
+        ws = _want("workspace", workspace, torch.uint8, (n,), self._dev) if n else None
+        self._check(self._lib.oasis_q8_attn(self.q8, R, S, 1 if causal else 0, qp, typ, table, lens, o, ws, n, st))
+
+    def _scratch_on(self, n: int, stream) -> torch.Tensor:
+        if stream is None:
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def oasis_prefix_workspace(self, R: int, S: int, prefix_len: int) -> int:
         n = c_size_t(0)

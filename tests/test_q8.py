@@ -442,6 +442,140 @@ def test_long_context_many_splits(dev):
     close(out, o, b)
 
 
+# ------------------------------------- attention with requests cut into parts
+def wide(lens, Hkv, G, dtype, fp32, g, least=7000):
+    """A cache whose table is wide enough that attention over the batch cuts requests into parts."""
+    R = len(lens)
+    nb = max(4 * -(-least // (R * Hkv)), max(-(-n // 16) for n in lens), 4 * 32 * 16 if R == 1 else 0)
+    c = cache_of(sum(-(-n // 16) for n in lens) + 3, nb, G * Hkv, Hkv, out_fp32=fp32)
+    pages = fill(c, g, spread=1.0)
+    return c, pages, Q.table_of(lens, c.cfg.num_pages, nb, g)
+
+
+@pytest.mark.parametrize("lens", [[1], [0], [700], [0, 0], [64, 0, 65], [3000, 5], [16, 255, 256, 257, 1024, 1025, 0, 2],
+                                  list(range(0, 128 * 9, 9)), list(range(33))], ids=lambda x: f"{len(x)}x{max(x)}")
+@pytest.mark.parametrize("S,causal,Hkv,G,dtype,fp32", [(1, False, 2, 4, BF, True), (4, True, 2, 4, HF, True),
+                                                       (2, False, 1, 5, BF, False), (4, True, 1, 8, HF, False),
+                                                       (3, True, 3, 1, BF, True)])
+def test_attention_in_parts(dev, lens, S, causal, Hkv, G, dtype, fp32):
+    g = gen(sum(lens) + S)
+    R = len(lens)
+    c, pages, table = wide(lens, Hkv, G, dtype, fp32, g)
+    n = c.oasis_q8_attn_workspace(R, S)
+    if R * Hkv <= 128:
+        assert n > 0
+    q = (2 * torch.randn(S, R, G * Hkv, 128, generator=g)).to(dtype).cuda()
+    o, b = Q.attention(q.cpu(), pages, table.numpy(), lens, causal, out=FP if fp32 else dtype)
+    close(attend(c, q, table, lens, causal), o, b)
+    # whatever the scratch holds, and nothing behind it is touched
+    ws = torch.full((n + 256,), 0xFF, dtype=torch.uint8, device=dev)
+    out = torch.full(q.shape, 5.0, dtype=FP if fp32 else dtype, device=dev)
+    t, m = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    c.oasis_q8_attn(q, t, m, out, causal=causal, workspace=ws)
+    close(out, o, b)
+    assert (ws[n:] == 0xFF).all()
+    # and without: in one piece
+    c.oasis_q8_attn(q, t, m, out, causal=causal, workspace=ws[:0])
+    close(out, o, b)
+    assert c.oasis_q8_sync() == 0
+
+
+def test_parts_lengths_and_pages_that_are_wrong(dev):
+    """A length past the table is cut to it, a negative one is empty, tokens of bad pages are left
+    out; each raises its bit but the negative one."""
+    g = gen(41)
+    lens = [40, 2000, 90]
+    c, pages, table = wide(lens, 2, 4, BF, True, g)
+    q = torch.randn(2, 3, 8, 128, generator=g).to(BF)
+    out = attend(c, q.cuda(), table, [40, -5, -2 ** 31], False)
+    assert c.oasis_q8_sync() == 0
+    o, b = Q.attention(q, pages, table.numpy(), [40, 0, 0], False, out=FP)
+    close(out, o, b)
+    bad = table.clone()
+    bad[1, 125 // 2:] = c.cfg.num_pages                 # the second request's last half and all behind
+    out = attend(c, q.cuda(), bad, [40, 2000, 90], False)
+    with pytest.raises(ob.OasisError) as e:
+        c.oasis_q8_sync()
+    assert "0x1" in str(e.value)
+    o, b = Q.attention(q, pages, table.numpy(), [40, 125 // 2 * 16, 90], False, out=FP)
+    close(out, o, b)
+    wide_table = torch.full((3, c.cfg.max_blocks), -1, dtype=torch.int32)
+    wide_table[:, :8] = table[1, :8]
+    out = attend(c, q.cuda(), wide_table, [2 ** 31 - 1, 128, 16 * c.cfg.max_blocks + 1], False)
+    with pytest.raises(ob.OasisError):
+        c.oasis_q8_sync()
+    o, b = Q.attention(q, pages, wide_table.numpy(), [128, 128, 128], False, out=FP)
+    close(out, o, b)
+
+
+def test_parts_workspace_refusals(dev):
+    g = gen(42)
+    lens = [40, 2000, 90]
+    c, pages, table = wide(lens, 2, 4, BF, False, g)
+    q = torch.randn(1, 3, 8, 128, generator=g).to(BF).cuda()
+    n = c.oasis_q8_attn_workspace(3, 1)
+    t, m = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    ws = torch.zeros(n + 256, dtype=torch.uint8, device=dev)
+    for bad, err in [(ws[:n - 1], ob.OasisError), (ws[16:16 + n], ob.OasisError), (ws.view(torch.int32), ValueError),
+                     (ws.cpu(), ValueError), (ws[::2], ValueError)]:
+        with pytest.raises(err):
+            c.oasis_q8_attn(q, t, m, torch.empty_like(q), workspace=bad)
+    for args in [(-1, 1), (65536, 1), (1, 0), (1, 5)]:
+        with pytest.raises(ob.OasisError):
+            c.oasis_q8_attn_workspace(*args)
+    assert c.oasis_q8_attn_workspace(129, 1) == 0 and c.oasis_q8_attn_workspace(0, 1) == 0
+
+
+def test_parts_on_streams_and_in_graphs(dev):
+    """Calls that take their own scratch: eager on two streams at once, and two captured graphs
+    replayed side by side, all the same bytes as one by one."""
+    g = gen(43)
+    lens = [1500, 3, 0, 700]
+    c, pages, table = wide(lens, 2, 4, BF, True, g)
+    assert c.oasis_q8_attn_workspace(4, 3) > 0
+    t, m = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    qs = [torch.randn(3, 4, 8, 128, generator=g).to(BF).cuda() for _ in range(2)]
+    want = []
+    for q in qs:
+        o = torch.empty(q.shape, dtype=FP, device=dev)
+        c.oasis_q8_attn(q, t, m, o, causal=True)
+        torch.cuda.synchronize()
+        want.append(o)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty(3, 4, 8, 128, dtype=FP, device=dev) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        c.oasis_q8_attn(qs[0], t, m, outs[0], causal=True, stream=streams[0])
+        c.oasis_q8_attn(qs[1], t, m, outs[1], causal=True, stream=streams[1].cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(outs, want))
+    graphs = []
+    for q, o in zip(qs, outs):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            for _ in range(3):
+                c.oasis_q8_attn(q, t, m, o, causal=True)
+        graphs.append(gr)
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(outs, want))
+    # the lengths are the device's, read at each replay
+    m.copy_(torch.tensor([20, 900, 1, 0], dtype=torch.int32))
+    table2 = Q.table_of([20, 900, 1, 0], c.cfg.num_pages, c.cfg.max_blocks, g)
+    t.copy_(table2)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    o, b = Q.attention(qs[0].cpu(), pages, table2.numpy(), [20, 900, 1, 0], True, out=FP)
+    close(outs[0], o, b)
+    assert c.oasis_q8_sync() == 0
+
+
 # ---------------------------------------------------------------- prefix
 def prefix_of(g, Hkv, blocks, plen, garbage=True):
     x = torch.randn(Hkv, blocks, 2, 16, 128, generator=g).to(BF)

@@ -57,8 +57,9 @@ def test_null_and_misaligned_arguments():
         assert h.value is None
     assert L.oasis_q8_write(None, 16, 16, 0, 256, 256, 16, 1, None) == ob.OASIS_EINVAL
     assert L.oasis_q8_read(None, 1, 16, 16, 16, 0, 1, None) == ob.OASIS_EINVAL
-    assert L.oasis_q8_attn(None, 1, 1, 0, 16, 0, 16, 16, 16, None) == ob.OASIS_EINVAL
+    assert L.oasis_q8_attn(None, 1, 1, 0, 16, 0, 16, 16, 16, None, 0, None) == ob.OASIS_EINVAL
     assert L.oasis_prefix_attn(None, 1, 1, 0, 16, 0, 16, 1, 1, 16, 16, 16, None, 0, None) == ob.OASIS_EINVAL
+    assert L.oasis_q8_attn_workspace(None, 1, 1, None) == ob.OASIS_EINVAL
     assert L.oasis_prefix_workspace(None, 1, 1, 1, None) == ob.OASIS_EINVAL
     assert L.oasis_q8_sync(None, None) == ob.OASIS_EINVAL
     assert L.oasis_q8_set_wait_limit(None, 5) == ob.OASIS_EINVAL
