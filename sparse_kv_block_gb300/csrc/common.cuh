@@ -156,8 +156,8 @@ __device__ __forceinline__ uint32_t remote_smem(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
   return at;
 }
-__device__ __forceinline__ void store_remote(const double* p, uint32_t rank, double v) {
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote_smem(p, rank)), "d"(v) : "memory");
+__device__ __forceinline__ void store_remote(const void* p, uint32_t rank, uint64_t v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote_smem(p, rank)), "l"(v) : "memory");
 }
 __device__ __forceinline__ float load_remote(const float* p, uint32_t rank) {
   float v;

@@ -10,9 +10,9 @@
 // place of 32 bits can name another token (a vocabulary's neighbouring
 // borders are about 1e-5 apart).  The sums are therefore held to about 48
 // bits: pairs of floats (an error-free sum and its remainder, as Dekker and
-// Knuth give them), two entries an instruction, and 64 bits between segments
-// of the row.  64-bit arithmetic throughout would bound the kernel: the card's
-// rate for it is two lanes a clock and SM.
+// Knuth give them), two entries an instruction within a segment of the row.
+// 64-bit arithmetic would bound the kernel: the card's rate for it is two
+// lanes a clock and SM.
 //
 // One cluster of CTAs per request reads the one or two rows that are needed
 // once, segment by segment; the segments' sums go to every CTA through
@@ -32,35 +32,61 @@ constexpr int kThreads = kVerifyWarps * 32;
 constexpr int kMaxSegs = 1024;        // of 1024 entries: vocabularies up to 2^20
 constexpr int kShortSeg = 256, kLongSeg = 1024;
 
-// ---- four consecutive entries as floats, whatever the alignment
-template <typename T, bool kVec>
-__device__ __forceinline__ float4 row4(const T* p, int at, int V);
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ float4 row4(const T* p, int at, int V) {
-  if (kVec && at + 4 <= V) {
-    if constexpr (sizeof(T) == 4) {
-      return *reinterpret_cast<const float4*>(p + at);
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(p + at);
-      T t[4];
-      memcpy(t, &w, 8);
-      return make_float4(to_f(t[0]), to_f(t[1]), to_f(t[2]), to_f(t[3]));
-    }
+// ---- four consecutive entries, of any alignment, or with 0 past the row's end
+template <typename T>
+struct alignas(4 * sizeof(T)) Four {
+  T x[4];
+};
+// As floats.  (Of bf16 by shifts: conversions run at a quarter of the rate.)
+__device__ __forceinline__ void floats_of(const Four<float>& f, float (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = f.x[i];
+}
+__device__ __forceinline__ void floats_of(const Four<__nv_bfloat16>& f, float (&x)[4]) {
+  uint32_t w[2];
+  memcpy(w, f.x, 8);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[2 * i] = bf16lo(w[i]);
+    x[2 * i + 1] = bf16hi(w[i]);
   }
-  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (at < V) r.x = to_f(p[at]);
-  if (at + 1 < V) r.y = to_f(p[at + 1]);
-  if (at + 2 < V) r.z = to_f(p[at + 2]);
-  if (at + 3 < V) r.w = to_f(p[at + 3]);
+}
+__device__ __forceinline__ void floats_of(const Four<__half>& f, float (&x)[4]) {
+  __half2 w[2];
+  memcpy(w, f.x, 8);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 v = __half22float2(w[i]);
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
+  }
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ Four<T> row4(const T* p) {
+  if constexpr (kVec) {
+    return *reinterpret_cast<const Four<T>*>(p);
+  } else {
+    Four<T> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.x[i] = p[i];
+    return r;
+  }
+}
+template <typename T>
+__device__ __forceinline__ Four<T> row4(const T* p, int at, int V) {
+  Four<T> r;
+  const T none = T(0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.x[i] = at + i < V ? p[at + i] : none;
   return r;
 }
 
 // ---- sums of pairs: hi + lo, hi the rounded sum (no contraction: __f*_rn)
-struct Pair {
+struct alignas(8) Pair {
   float hi, lo;
 };
 __device__ __forceinline__ Pair join(Pair s, Pair x) {
@@ -69,8 +95,16 @@ __device__ __forceinline__ Pair join(Pair s, Pair x) {
   const float e = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, z)), __fsub_rn(x.hi, z));
   return {t, __fadd_rn(s.lo, __fadd_rn(e, x.lo))};
 }
-__device__ __forceinline__ double value(Pair a) {
-  return static_cast<double>(a.hi) + static_cast<double>(a.lo);
+// The same with lo under half a unit of hi again, for the long chains.
+__device__ __forceinline__ Pair join_tight(Pair s, Pair x) {
+  const Pair t = join(s, x);
+  const float hi = __fadd_rn(t.hi, t.lo);
+  return {hi, __fsub_rn(t.lo, __fsub_rn(hi, t.hi))};
+}
+// a < b.
+__device__ __forceinline__ bool less(Pair a, Pair b) {
+  const Pair d = join(b, Pair{-a.hi, -a.lo});
+  return __fadd_rn(d.hi, d.lo) > 0.f;
 }
 // max(p - q, 0) exactly, negative numbers and NaN counting as 0: with the
 // larger of the two first, the remainder of the difference takes three steps.
@@ -111,33 +145,112 @@ __device__ __forceinline__ Pair scan(Pair a, int lane) {
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const Pair o = {__shfl_up_sync(0xffffffffu, a.hi, off), __shfl_up_sync(0xffffffffu, a.lo, off)};
-    if (lane >= off) a = join(o, a);
+    if (lane >= off) a = join_tight(o, a);
   }
   return a;
 }
 
 // What a request's threshold falls on.
-template <typename T, bool kVec>
+template <typename T>
 struct Rows {
   const T* p;
   const T* q;      // null: nothing to subtract
   int certain;     // the token that a certain draft takes out, or -1
   int V;
-  __device__ __forceinline__ void load(int at, float4& x, float4& y) const {
-    x = row4<T, kVec>(p, at, V);
-    y = q ? row4<T, kVec>(q, at, V) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (certain >= at && certain < at + 4) {
-      x.x = certain == at ? 0.f : x.x;
-      x.y = certain == at + 1 ? 0.f : x.y;
-      x.z = certain == at + 2 ? 0.f : x.z;
-      x.w = certain == at + 3 ? 0.f : x.w;
+};
+
+// A warp's sums over a segment's entries, each lane its own.
+template <typename T, bool kVec, int kSeg, bool kQ>
+__device__ __forceinline__ Pair segment(const Rows<T>& rows, int seg, int lane) {
+  const uint64_t minus = f2pack(-1.f, -1.f);
+  Pair2 s0{}, s1{};
+  auto add = [&](int at, const Four<T>& from, const Four<T>& less) {
+    float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+    floats_of(from, x);
+    if constexpr (kQ) {
+      floats_of(less, y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = rows.certain == at + i ? 0.f : x[i];
+    }
+    add_rest2(s0, x[0], x[1], y[0], y[1], minus);
+    add_rest2(s1, x[2], x[3], y[2], y[3], minus);
+  };
+  const int begin = seg * kSeg + lane * 4;
+  constexpr int kLoads = kSeg / 128;
+  if ((seg + 1) * kSeg <= rows.V) {
+    // Nothing between the loads, so that a batch is in flight together.  (With
+    // a test for the row's end at each load the code waits between them: 128
+    // rows of 151936 took 28.3 us in fp32 and 40 in bf16 instead of 24 and 21.)
+    constexpr int kBatch = kLoads < 4 ? kLoads : 4;
+#pragma unroll
+    for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
+      Four<T> x[kBatch], y[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        x[i] = row4<T, kVec>(rows.p + begin + (i0 + i) * 128);
+        if constexpr (kQ) y[i] = row4<T, kVec>(rows.q + begin + (i0 + i) * 128);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) add(begin + (i0 + i) * 128, x[i], y[i]);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = begin + i * 128;
+      Four<T> x, y;
+      x = row4<T>(rows.p, at, rows.V);
+      if constexpr (kQ) y = row4<T>(rows.q, at, rows.V);
+      add(at, x, y);
     }
   }
+  return join(join(half_of(s0, 0), half_of(s0, 1)), join(half_of(s1, 0), half_of(s1, 1)));
+}
+
+// The segment that u of the total falls in, and what of it the segment has to
+// exceed; -1 where there is nothing, -2 where there is no sum.  By one warp: the
+// sums before each lane's share of the segments, then the segments of one
+// share.  (64-bit operations took as long as this in pairs, 1 us alone and 3
+// beside another CTA that reads; run ahead on a made-up table, to have the code
+// at hand, it cost 3 us.)
+struct Found {
+  int seg;
+  Pair rest;
 };
+__device__ __noinline__ Found find(const Pair* sums, int segs, float u, int lane) {
+  const int share = (segs + 31) / 32;
+  Pair own{};
+  for (int i = 0; i < share; ++i)
+    if (lane * share + i < segs) own = join_tight(own, sums[lane * share + i]);
+  const Pair incl = scan(own, lane);
+  const Pair total = {__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
+  Found f = {total.hi == 0.f ? -1 : -2, {}};
+  if (!(total.hi > 0.f && total.hi + total.lo < INFINITY)) return f;
+  const float high = __fmul_rn(u, total.hi);
+  const Pair threshold = {high, __fmaf_rn(u, total.lo, __fmaf_rn(u, total.hi, -high))};
+  // The lane whose share holds it; past the end (u = 1, or a rounding), the
+  // last lane with anything.
+  const unsigned over = __ballot_sync(0xffffffffu, own.hi > 0.f && less(threshold, incl));
+  const unsigned some = __ballot_sync(0xffffffffu, own.hi > 0.f);
+  const int at = over ? __ffs(over) - 1 : 31 - __clz(some);
+  Pair before = {__shfl_up_sync(0xffffffffu, incl.hi, 1), __shfl_up_sync(0xffffffffu, incl.lo, 1)};
+  if (lane == 0) before = Pair{};
+  before = {__shfl_sync(0xffffffffu, before.hi, at), __shfl_sync(0xffffffffu, before.lo, at)};
+  for (int i = 0; i < share && at * share + i < segs; ++i) {
+    const Pair v = sums[at * share + i];
+    if (v.hi > 0.f) {
+      f.seg = at * share + i;
+      f.rest = join(threshold, Pair{-before.hi, -before.lo});
+      if (less(f.rest, v)) break;
+    }
+    before = join_tight(before, v);
+  }
+  return f;
+}
 
 template <typename T, bool kVec, int kSeg>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a, int cluster) {
-  __shared__ double sums[2][kMaxSegs];
+  __shared__ Pair sums[2][kMaxSegs];
   __shared__ int first_s, bad_s, seg_s, last_s;
   __shared__ Pair target_s;            // the threshold, from its segment's start
   __shared__ Pair warp_sum[kVerifyWarps];
@@ -153,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
                            : nullptr;
   const int32_t* tokens = a.tokens + static_cast<int64_t>(r) * a.n;
   int32_t* out = a.out_tokens + static_cast<int64_t>(r) * (a.n + 1);
+  const float u = a.u_sample[r];
 
   // The first refused draft.  Products of two floats are exact in 64 bits.
   if (tid == 0) {
@@ -162,13 +276,13 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
     const int x = tokens[i];
-    const float u = a.u_accept[static_cast<int64_t>(r) * a.n + i];
+    const float ua = a.u_accept[static_cast<int64_t>(r) * a.n + i];
     if (x < 0 || x >= V) {
       bad_s = 1;
     } else {
       const float p = fmaxf(to_f(target[i * a.target_stride + x]), 0.f);
       const float q = draft ? fmaxf(to_f(draft[i * a.draft_stride + x]), 0.f) : 1.f;
-      if (!(static_cast<double>(u) * static_cast<double>(q) < static_cast<double>(p))) atomicMin(&first_s, i);
+      if (!(static_cast<double>(ua) * static_cast<double>(q) < static_cast<double>(p))) atomicMin(&first_s, i);
     }
   }
   cluster_sync();  // also: every CTA runs before the first remote store
@@ -181,77 +295,29 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a,
   }
   if (bad) return;  // every CTA of the cluster alike
 
-  Rows<T, kVec> rows;
+  Rows<T> rows;
   rows.p = target + k * a.target_stride;
   rows.q = k < n && draft ? draft + k * a.draft_stride : nullptr;
   rows.certain = k < n && !draft ? tokens[k] : -1;
   rows.V = V;
   const int segs = (V + kSeg - 1) / kSeg;
   const int stride = cluster * kVerifyWarps;
-  const uint64_t minus = f2pack(-1.f, -1.f);
   for (int pass = 0; pass < 2; ++pass) {
-    double* mine = sums[pass];
-    for (int seg = rank * kVerifyWarps + warp; seg < segs; seg += stride) {
-      Pair2 s0{}, s1{};
-      constexpr int kLoads = kSeg / 128, kBatch = kLoads < 4 ? kLoads : 4;
-#pragma unroll
-      for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
-        float4 x[kBatch], y[kBatch];  // in flight together
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) rows.load(seg * kSeg + (i0 + i) * 128 + lane * 4, x[i], y[i]);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          add_rest2(s0, x[i].x, x[i].y, y[i].x, y[i].y, minus);
-          add_rest2(s1, x[i].z, x[i].w, y[i].z, y[i].w, minus);
-        }
-      }
-      Pair t = join(join(half_of(s0, 0), half_of(s0, 1)), join(half_of(s1, 0), half_of(s1, 1)));
+    Pair* mine = sums[pass];
+    for (int at = rank * kVerifyWarps + warp; at < segs; at += stride) {
+      Pair t = rows.q ? segment<T, kVec, kSeg, true>(rows, at, lane) : segment<T, kVec, kSeg, false>(rows, at, lane);
 #pragma unroll
       for (int off = 16; off; off >>= 1) t = join(t, shuffled(t, off));
       t = {__shfl_sync(0xffffffffu, t.hi, 0), __shfl_sync(0xffffffffu, t.lo, 0)};
-      if (lane < cluster) store_remote(&mine[seg], lane, value(t));
+      if (lane < cluster) store_remote(&mine[at], lane, f2pack(t.hi, t.lo));
     }
     cluster_sync();
 
-    // One warp: the sums before each lane's share of the segments, the total,
-    // and the segment that the threshold falls in.  (64-bit operations of all
-    // warps would queue for the same two lanes.)
     if (warp == 0) {
-      const int share = (segs + 31) / 32;
-      double own = 0.0;
-      for (int i = 0; i < share; ++i)
-        if (lane * share + i < segs) own += mine[lane * share + i];
-      double incl = own;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
-      }
-      const double total = __shfl_sync(0xffffffffu, incl, 31);
-      int seg = total == 0.0 ? -1 : -2;  // nothing there; no sum
-      double rest_of = 0.0;
-      if (total > 0.0 && total < INFINITY) {
-        const double threshold = static_cast<double>(a.u_sample[r]) * total;
-        // The lane whose share holds it; past the end (u = 1, or a rounding),
-        // the last lane with anything.
-        const unsigned over = __ballot_sync(0xffffffffu, incl > threshold && own > 0.0);
-        const unsigned some = __ballot_sync(0xffffffffu, own > 0.0);
-        const int at = over ? __ffs(over) - 1 : 31 - __clz(some);
-        double before = __shfl_sync(0xffffffffu, incl - own, at);
-        for (int i = 0; i < share && at * share + i < segs; ++i) {
-          const double v = mine[at * share + i];
-          if (v > 0.0) {
-            seg = at * share + i;
-            rest_of = threshold - before;
-            if (rest_of < v) break;
-          }
-          before += v;
-        }
-      }
+      const Found f = find(mine, segs, u, lane);
       if (lane == 0) {
-        seg_s = seg;
-        target_s.hi = static_cast<float>(rest_of);
-        target_s.lo = static_cast<float>(rest_of - static_cast<double>(target_s.hi));
+        seg_s = f.seg;
+        target_s = f.rest;
         first_s = 0x7fffffff;
         last_s = -1;
       }

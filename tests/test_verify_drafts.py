@@ -46,7 +46,7 @@ def draw(R, n, V, g, dtype=FP, temp=2.0, noise=0.7):
 
 @pytest.mark.parametrize("dtype", [FP, BF, HF])
 @pytest.mark.parametrize("R,n,V", [(1, 1, 1), (2, 0, 7), (3, 2, 31), (1, 3, 1023), (40, 3, 1024), (5, 6, 1025),
-                                   (2, 4, 32000), (64, 3, 5003), (170, 2, 2500), (3, 3, 151936), (1, 64, 300)])
+                                   (2, 4, 32000), (64, 3, 5003), (170, 2, 2500), (3, 3, 151936), (1, 64, 300), (270, 1, 9001)])
 def test_against_definition(dev, dtype, R, n, V):
     p, q, x, ua, us = draw(R, n, V, gen(R * 1000 + V + n), dtype)
     for d in (q, None):
