@@ -766,14 +766,16 @@ cudaError_t launch_split(const Q8AttnArgs& a, int warps, cudaStream_t s) {
 // launch) and gains where lengths differ or pairs are few: one round of CTAs of
 // about one size fills the card, where a cluster ends at eight CTAs and keeps
 // the room of those that a short request leaves idle.  So: where the card holds
-// at least 1.7 CTAs a pair, and there are either 7000 groups of unequal
-// requests, or eight groups a warp fewer.  GB300, us without and with (8 KV
-// heads of four query heads, lengths uniform up to the given one; in brackets
-// four queries): 2 x 131072 118, 84 [157, 87]; 2 x 32000 34, 25 [46, 32];
-// 5 x 30000 32, 27 [38, 35.5]; 24 x 9001 51.5, 49.5 [74, 61]; 38 x 8192 [94, 80];
-// 20 x 3000 22, 20.5 [39, 28]; one of 131072 104, 57 [140, 59], of 32768 30, 22
-// [43, 26].  But 20 x 2000 18, 19; 8 x 4000 16, 18; and where rounds are needed
-// 100 x 4000 81, 83 [111, 121].
+// at least 1.7 CTAs a pair, and in clusters a warp of the longest request has
+// seven groups or more (of a single one, eight more than in parts).  GB300, us
+// without and with (8 KV heads of four query heads, lengths uniform up to the
+// given one; in brackets four queries): 2 x 131072 118, 84 [157, 87]; 2 x 32000
+// 34, 25 [46, 32]; 5 x 30000 32, 27 [38, 35.5]; 24 x 9001 51.5, 49.5 [74, 61];
+// 38 x 8192 [94, 80]; 16 x 4000 25.5, 22 [32, 30]; 24 x 3000 [39, 28]; 6 x 8000
+// [31, 25]; one of 131072 104, 57 [140, 59], of 32768 30, 22 [43, 26].  But, not
+// cut, 8 x 4000 16, 18 [21, 25]; 24 x 2000 17.5, 19.5; where rounds are needed
+// 100 x 4000 81, 83 [111, 121].  Equal lengths lose near the bound (16 x 4000
+// 29, 32 [34, 41]) and nothing further on (24 x 3000 [42, 43]).
 Q8Split q8_split(int R, int S, int G, int Hkv, int max_blocks) {
   Q8Split p{};
   if (R < 1 || R > kSplitRequests) return p;
@@ -792,7 +794,7 @@ Q8Split q8_split(int R, int S, int G, int Hkv, int max_blocks) {
   while (cluster < 8 && pairs * cluster * 2 <= 152 * CTAs) cluster *= 2;
   const int64_t whole = groups / (cluster * 4);
   const int64_t part = pairs * groups / (slots * p.warps);
-  const bool gains = (R > 1 && pairs * groups >= 7000) || whole >= (part > kLeastGroups ? part : kLeastGroups) + 8;
+  const bool gains = whole >= (R > 1 ? 7 : (part > kLeastGroups ? part : kLeastGroups) + 8);
   if (!gains) return p;
   p.columns = static_cast<int>(slots / (static_cast<int64_t>(Hkv) * col_groups));
   const int64_t rows = static_cast<int64_t>(p.columns) * Hkv * cols;

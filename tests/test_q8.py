@@ -446,7 +446,7 @@ def test_long_context_many_splits(dev):
 def wide(lens, Hkv, G, dtype, fp32, g, least=7000):
     """A cache whose table is wide enough that attention over the batch cuts requests into parts."""
     R = len(lens)
-    nb = max(4 * -(-least // (R * Hkv)), max(-(-n // 16) for n in lens), 4 * 32 * 16 if R == 1 else 0)
+    nb = max(4 * -(-least // (R * Hkv)), max(-(-n // 16) for n in lens), 4 * 32 * 16 if R == 1 else 4 * 256)
     c = cache_of(sum(-(-n // 16) for n in lens) + 3, nb, G * Hkv, Hkv, out_fp32=fp32)
     pages = fill(c, g, spread=1.0)
     return c, pages, Q.table_of(lens, c.cfg.num_pages, nb, g)
