@@ -766,7 +766,8 @@ cudaError_t launch_split(const Q8AttnArgs& a, int warps, cudaStream_t s) {
 // launch) and gains where lengths differ or pairs are few: one round of CTAs of
 // about one size fills the card, where a cluster ends at eight CTAs and keeps
 // the room of those that a short request leaves idle.  So: where the card holds
-// at least 1.7 CTAs a pair, and in clusters a warp of the longest request has
+// at least 1.7 CTAs a pair (of two warps with two column tiles), and in
+// clusters a warp of the longest request has
 // seven groups or more (of a single one, eight more than in parts).  GB300, us
 // without and with (8 KV heads of four query heads, lengths uniform up to the
 // given one; in brackets four queries): 2 x 131072 118, 84 [157, 87]; 2 x 32000
@@ -775,27 +776,35 @@ cudaError_t launch_split(const Q8AttnArgs& a, int warps, cudaStream_t s) {
 // [31, 25]; one of 131072 104, 57 [140, 59], of 32768 30, 22 [43, 26].  But, not
 // cut, 8 x 4000 16, 18 [21, 25]; 24 x 2000 17.5, 19.5; where rounds are needed
 // 100 x 4000 81, 83 [111, 121].  Equal lengths lose near the bound (16 x 4000
-// 29, 32 [34, 41]) and nothing further on (24 x 3000 [42, 43]).
+// 29, 32 [34, 41]) and nothing further on (24 x 3000 [42, 43]).  Rounds are
+// taken with two column tiles, up to two of them, from 48 groups on: [64 x 16384
+// 239, 200; equal 371, 379]; below it is [64 x 8192 131, 130; equal 197, 221].
 Q8Split q8_split(int R, int S, int G, int Hkv, int max_blocks) {
   Q8Split p{};
   if (R < 1 || R > kSplitRequests) return p;
   const int cols = S * G, col_groups = (cols + 15) / 16, CTAs = cols <= 8 ? 3 : 2;
   const int64_t pairs = static_cast<int64_t>(R) * Hkv * col_groups;
   const int64_t groups = (max_blocks + kGroupUnits - 1) / kGroupUnits;
-  // Two warps a CTA with two column tiles where parts of four would be a
-  // quarter of a pair or more: 24 x 9001 65, 61 us with four, two; 40 x 4000
-  // 64, 56; but 5 x 30000 35, 38, one of 131072 59, 66.
-  const bool fine = cols > 8 && pairs * 4 > 152 * CTAs;
-  p.warps = fine ? 2 : 4;
-  const int64_t slots = 152 * CTAs * (fine ? 2 : 1);
-  if (pairs * 17 > slots * 10) return p;
-  // Groups of a warp at the longest: in clusters (as launch_t takes them), in parts.
+  const int64_t fit = 152 * CTAs;  // CTAs of four warps that the card holds
+  // Groups of a warp at the longest, in clusters (as launch_t takes them).
   int64_t cluster = 1;
-  while (cluster < 8 && pairs * cluster * 2 <= 152 * CTAs) cluster *= 2;
+  while (cluster < 8 && pairs * cluster * 2 <= fit) cluster *= 2;
   const int64_t whole = groups / (cluster * 4);
-  const int64_t part = pairs * groups / (slots * p.warps);
-  const bool gains = whole >= (R > 1 ? 7 : (part > kLeastGroups ? part : kLeastGroups) + 8);
-  if (!gains) return p;
+  int64_t slots;
+  if (pairs * 17 <= fit * (cols > 8 ? 20 : 10)) {
+    // Two warps a CTA with two column tiles where parts of four would be a
+    // quarter of a pair or more: 24 x 9001 65, 61 us with four, two; 40 x 4000
+    // 64, 56; but 5 x 30000 35, 38, one of 131072 59, 66.
+    p.warps = cols > 8 && pairs * 4 > fit ? 2 : 4;
+    slots = fit * 4 / p.warps;
+    const int64_t part = pairs * groups / (slots * p.warps);
+    if (whole < (R > 1 ? 7 : (part > kLeastGroups ? part : kLeastGroups) + 8)) return p;
+  } else {
+    // In rounds.
+    if (cols <= 8 || pairs > 2 * fit || whole < 48) return p;
+    p.warps = 4;
+    slots = fit * ((2 * pairs + fit - 1) / fit);
+  }
   p.columns = static_cast<int>(slots / (static_cast<int64_t>(Hkv) * col_groups));
   const int64_t rows = static_cast<int64_t>(p.columns) * Hkv * cols;
   auto up = [](int64_t n) { return static_cast<size_t>((n + 255) / 256 * 256); };

@@ -480,6 +480,30 @@ def test_attention_in_parts(dev, lens, S, causal, Hkv, G, dtype, fp32):
     assert c.oasis_q8_sync() == 0
 
 
+@pytest.mark.parametrize("Hkv,lens", [(3, [(7 * i) % 431 for i in range(120)]), (2, [333, 1000, 31])],
+                         ids=["rounds", "one round"])
+def test_parts_behind_whose_ends_anything_stands(dev, Hkv, lens):
+    """What no query sees may be NaN codes and odd exponents, in parts too; 120 x 3 pairs take
+    rounds of CTAs."""
+    g = gen(44)
+    S, G = 4, 4
+    c, pages, table = wide(lens, Hkv, G, BF, True, g)
+    for r, n in enumerate(lens):
+        if n % 16:
+            u = pages[int(table[r, n // 16])]
+            for j in range(n % 16, 16):
+                u[:, Q.key_at(j, np.arange(128))] = 0x7F
+                u[:, Q.value_at(j, np.arange(128))] = 0xFF
+                u[:, [4096 + j, 4112 + j]] = 255 if j & 1 else 0
+    c.pages.copy_(torch.from_numpy(pages))
+    assert c.oasis_q8_attn_workspace(len(lens), S) > 0
+    q = (2 * torch.randn(S, len(lens), G * Hkv, 128, generator=g)).to(BF)
+    out = attend(c, q.cuda(), table, lens, True)
+    assert c.oasis_q8_sync() == 0
+    o, b = Q.attention(q, pages, table.numpy(), lens, True, out=FP)
+    close(out, o, b)
+
+
 def test_parts_lengths_and_pages_that_are_wrong(dev):
     """A length past the table is cut to it, a negative one is empty, tokens of bad pages are left
     out; each raises its bit but the negative one."""
