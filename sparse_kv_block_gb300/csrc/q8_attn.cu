@@ -701,15 +701,25 @@ cudaError_t launch_n(const Q8AttnArgs& a, cudaStream_t s) {
   // tokens 15.7, 15.5, 13.3; 300 x 16 x 100 66, 41, 37; 128 ragged ones up to
   // 500 23.3, 23.1, 24.4; with two tiles, 128 up to 300 40, 33; but 64 up to
   // 1000 19.8, 23.8.
-  // More than eight columns: a tile of eight a CTA where all is small, although
-  // the pages are then read again (from the L2): a warp's chain is shorter and
-  // the card is not full.  Four queries x four heads, us with two tiles a CTA
+  // More than eight columns: a tile of eight a CTA where all is small, or where
+  // contexts are short and it leaves a pair as many CTAs, although the pages
+  // are then read again (from the L2): a warp's chain is shorter and the card
+  // is not full.  Four queries x four heads, us with two tiles a CTA
   // and with one: 300 tokens x 8 heads 11.7, 9.8; 8 x 300 12.0, 9.6; 40 x 300
   // 19.3, 16.7; 8000 18.8, 16.3; but 16 x 1000 16.4, 16.8; 8 x 2000 15.8, 17.5;
-  // 4 x 4000 16.3, 18.7.
+  // 4 x 4000 16.3, 18.7.  As many CTAs: 20 x 777 17.6, 14.9; 24 x 1500 25.4, 22.6;
+  // 12 x 2000 21.1, 18.6.
   const int cols = a.S * a.G, groups = (a.max_blocks + kGroupUnits - 1) / kGroupUnits;
   const int64_t pairs = static_cast<int64_t>(a.R) * a.Hkv;
-  if (cols <= 8 || pairs * groups <= 1600) {
+  auto cluster = [](int64_t ctas, int64_t fit) {
+    int c = 1;
+    while (c < 8 && ctas * c * 2 <= fit) c *= 2;
+    return c;
+  };
+  const int64_t single = pairs * ((cols + 7) / 8);  // CTAs of one tile
+  if (cols <= 8 || pairs * groups <= 1600 ||
+      (groups <= 32 && single <= 3 * 152 &&
+       cluster(single, 3 * 152) >= cluster(pairs * ((cols + 15) / 16), 2 * 152))) {
     const int col_groups = (cols + 7) / 8;
     if (pairs * col_groups <= 3 * 152 || groups > 8) return launch_t<T, 4, 1>(a, col_groups, s);
     return groups > 4 ? launch_t<T, 2, 1>(a, col_groups, s) : launch_t<T, 1, 1>(a, col_groups, s);
