@@ -4,11 +4,11 @@
 //
 // One CTA, or one cluster of CTAs where there are few (request, KV head)
 // pairs, per pair; or, given scratch, as many CTAs a request as its length
-// asks for, joined by a second launch.  Every warp takes groups of 64 tokens (four units) through
-// a ring of its own, two bulk copies per unit (its keys; its values and
-// exponents).  The two products run on mma.sync m16n8k16 with tokens, then
-// dims, as M and up to 16 query columns (query s, head gi: column s * G + gi)
-// as N.  Codes become fp16 exactly;
+// asks for, joined by a second launch.  Every warp takes groups of 64 tokens
+// (four units) through a ring of its own, two bulk copies per unit (its keys;
+// its values and exponents).  The two products run on mma.sync m16n8k16 with
+// tokens, then dims, as M and up to 16 query columns (query s, head gi: column
+// s * G + gi) as N.  Codes become fp16 exactly;
 // which token stands for which matrix row is chosen so that a lane's 16-byte
 // loads are whole fragments and the transposed weights (movmatrix) meet the
 // value codes as they lie:
@@ -30,9 +30,6 @@
 #include "q8.cuh"
 #include "q8.h"
 
-#ifndef NOSPLIT
-#define NOSPLIT 0
-#endif
 namespace oasis {
 namespace {
 
