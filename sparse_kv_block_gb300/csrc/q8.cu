@@ -87,11 +87,18 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
   w[3] = __byte_perm(b, d, 0x7632);
 }
 
-// 32 bytes, a whole sector.
+// 32 bytes of a unit, 16-byte aligned: a whole sector in one store where they
+// are one, which the instruction requires (a unit's 4128 bytes are a multiple
+// of 32, so that is so for all of a pool's units or for none), else two.
 __device__ __forceinline__ void store32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 constexpr int kWriteWarps = 4;
