@@ -187,8 +187,10 @@ __global__ void __launch_bounds__(PrefixLayout<kTiles>::kThreads, 1)
     load_blocks(dst + kHalfTile, &map, 64, j & 1, block, h, &full[st]);
   };
   int loaded = 0;
-  if (warp == kTiles * 4 + 1) tmem_alloc(tmem_s, Lay::kColumns);
   previous_done();
+  // (Not before: a kernel ahead that takes tensor memory after it has let its
+  // dependents begin would wait for this one's.)
+  if (warp == kTiles * 4 + 1) tmem_alloc(tmem_s, Lay::kColumns);
   next_may_begin();  // the pages' share takes the SMs this leaves idle
   if (loader) {
     prefetch_tensormap(&map);
