@@ -292,20 +292,15 @@ __device__ __forceinline__ float2 values2(uint32_t codes, float s) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return make_float2(f.x * s, f.y * s);
 }
-__device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float2 f) { return pack_bf16x2(f.x, f.y); }
-__device__ __forceinline__ uint32_t pack2(const __half*, float2 f) {
-  const __half2 v = __floats2half2_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 // Four codes of a row and its scale -> four values at p.
 template <typename T>
 __device__ __forceinline__ void put4(T* p, uint32_t codes, float s) {
   const float2 a = values2(codes & 0xffffu, s), b = values2(codes >> 16, s);
   if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<float4*>(p) = make_float4(finite(a.x), finite(a.y), finite(b.x), finite(b.y));
   } else {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(p, a), pack2(p, b));
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2_finite(p, a.x, a.y), pack2_finite(p, b.x, b.y));
   }
 }
 

@@ -59,6 +59,23 @@ __device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d)
   return q8_pack2(a, b) | (q8_pack2(c, d) << 16);
 }
 
+// Two floats -> two of a 16-bit type, to nearest even; past its range the
+// largest of it, NaN stays NaN.  (What codes stand for is finite, but the
+// largest code a row's largest value rounds to can lie past the type's range.)
+__device__ __forceinline__ uint32_t pack2_finite(const __nv_bfloat16*, float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2_finite(const __half*, float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float finite(float x) {
+  return fabsf(x) == INFINITY ? copysignf(__uint_as_float(0x7f7fffffu), x) : x;
+}
+
 // Two e4m3 codes -> two halves (exact).
 __device__ __forceinline__ uint32_t q8_unpack2(uint32_t codes) {
   uint32_t r;
@@ -152,8 +169,13 @@ __device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
-__device__ __forceinline__ void store4(__half* p, const float4& v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+// An output over codes, which is finite or NaN.
+__device__ __forceinline__ void store4_finite(float* p, const float4& v) {
+  store4(p, make_float4(finite(v.x), finite(v.y), finite(v.z), finite(v.w)));
+}
+template <typename T>
+__device__ __forceinline__ void store4_finite(T* p, const float4& v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2_finite(p, v.x, v.y), pack2_finite(p, v.z, v.w));
 }
 
 }  // namespace oasis

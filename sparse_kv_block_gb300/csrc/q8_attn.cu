@@ -643,8 +643,8 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
     const float4 v = sum[j] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                                    : make_float4(acc[j].x / sum[j], acc[j].y / sum[j], acc[j].z / sum[j],
                                                  acc[j].w / sum[j]);
-    if (a.out_fp32) store4(static_cast<float*>(a.out) + at, v);
-    else store4(static_cast<T*>(a.out) + at, v);
+    if (a.out_fp32) store4_finite(static_cast<float*>(a.out) + at, v);
+    else store4_finite(static_cast<T*>(a.out) + at, v);
   }
   // Beside another launch that writes shares: who waits for this grid has to
   // have waited for that one.  One CTA does it for all (others would keep SMs
@@ -745,8 +745,8 @@ __global__ void __launch_bounds__(128) join_parts(const Q8AttnArgs a) {
   // What a query sees nothing of is 0.
   const float4 v = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                               : make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum);
-  if (a.out_fp32) store4(static_cast<float*>(a.out) + row * kHeadDim + lane * 4, v);
-  else store4(static_cast<T*>(a.out) + row * kHeadDim + lane * 4, v);
+  if (a.out_fp32) store4_finite(static_cast<float*>(a.out) + row * kHeadDim + lane * 4, v);
+  else store4_finite(static_cast<T*>(a.out) + row * kHeadDim + lane * 4, v);
 }
 
 template <typename T, int W, int kNT>

@@ -51,3 +51,41 @@ def test_pages_lent_at_any_multiple_of_sixteen_bytes(dev, dtype, off):  # noqa: 
         got = back[r].permute(0, 2, 1, 3, 4).reshape(H, 2, -1, 128)[:, :, :n].double().cpu().numpy()
         assert np.array_equal(got[:, 0], kk) and np.array_equal(got[:, 1], vv)
     assert (arena[:off] == 0xA5).all() and (arena[off + P * H * Q.UNIT:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, FP])
+def test_the_largest_values_come_back_finite(dev, dtype):  # noqa: F811
+    """A row's largest value can round up to a power of two past the type's range: it is read, and
+    attended to, as the type's largest value, within 2^-4 of what was written (half a step of e4m3;
+    the type's own rounding of the output is less than the 2^-8 that the largest value is nearer)."""
+    top = torch.finfo(dtype).max
+    x = torch.zeros(32, 1, 128, dtype=torch.float64)
+    x[:, 0, 0] = torch.linspace(0.5, 1.0, 32, dtype=torch.float64) * top
+    x[:, 0, 1] = -x[:, 0, 0].flip(0)
+    x[:, 0, 2] = top
+    x[7, 0, 3], x[8, 0, 3], x[9, 0, 4] = float("inf"), float("-inf"), float("nan")
+    x = x.to(dtype)
+    c = ob.Q8Cache(ob.make_q8_config(2, 1, 2, 1, out_fp32=dtype == FP))
+    k = torch.zeros_like(x)
+    k[:, 0, :] = 1.0
+    c.oasis_q8_write(k.cuda(), x.cuda(), torch.arange(32).cuda())
+    out = torch.zeros(2, 1, 1, 2, 16, 128, dtype=dtype, device=dev)
+    c.oasis_q8_read(torch.tensor([[0], [1]], dtype=torch.int32).cuda(), torch.full((2,), 16, dtype=torch.int32).cuda(), out)
+    back = out[:, 0, 0, 1].reshape(32, 128).double().cpu()
+    want = x[:, 0].double()
+
+    def near(got, want):
+        fin = torch.isfinite(want)
+        assert torch.isfinite(got[~torch.isnan(want)]).all() and torch.isnan(got[torch.isnan(want)]).all()
+        assert ((got - want).abs()[fin] <= 2.0 ** -4 * want.abs()[fin]).all()
+    near(back, want)
+    assert back[7, 3] > 0 > back[8, 3] and back[7, 3].abs() == top and back[8, 3].abs() == top
+    # one token a request: its value is the output
+    qt = HF if dtype == HF else BF
+    for t in range(0, 32, 16):
+        pages = torch.full((2, 1), t // 16, dtype=torch.int32)
+        q = torch.ones(1, 2, 2, 128, dtype=qt).cuda()
+        got = attend(c, q, pages, [1, 0], False).double().cpu()
+        near(got[0, 0, 0].view(1, -1), want[t:t + 1])
+        assert (got[0, 1] == 0).all()
+    assert c.oasis_q8_sync() == 0
