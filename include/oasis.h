@@ -727,7 +727,9 @@ OASIS_API int oasis_prefix_workspace(const oasis_q8* q8, int num_requests, int n
  * (16-byte aligned; one request's units, e.g. from oasis_q8_read), then its
  * request's pages as above (seq_len counts those alone).  The prefix is read
  * once for the whole batch.  q must be bf16.  prefix_len <= 16 *
- * prefix_blocks; 0 is oasis_q8_attn. */
+ * prefix_blocks; 0 is oasis_q8_attn.  Weighted values are summed in fp32
+ * before they are divided, weights up to 2^8: the sums stay in range for
+ * values of magnitudes under 2^98, the prefix's and the pages'. */
 OASIS_API int oasis_prefix_attn(oasis_q8* q8, int num_requests, int num_queries, int causal,
                                 const void* q, int type, const void* prefix_kv,
                                 int prefix_blocks, int prefix_len, const int32_t* page_table,

@@ -37,6 +37,11 @@ constexpr int kGroupUnits = 4;
 constexpr int kGroupTokens = kGroupUnits * kBlock;           // 64
 constexpr int kGroupBytes = kGroupUnits * kQ8UnitBytes;      // 16512
 constexpr float kWeightLog2 = 14.f;
+// Sums of weighted values are kept in units of 2^22 once in the sum's units: a
+// request has up to 2^21 tokens of up to 448 * 2^120, and 2^21 * 2^129 / 2^22
+// is in fp32's range, as the output is, an average.  (A power of two, so no
+// bits change.)
+constexpr float kSumDown = 0x1p-22f, kSumUp = 0x1p22f;
 constexpr int kSplitRequests = 128;  // requests of a batch that can be cut into parts
 constexpr int kLeastGroups = 4;      // of a part's warp
 
@@ -75,6 +80,12 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) 
 }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+
+// The output of sums in units of 2^22; what a query sees nothing of is 0.
+__device__ __forceinline__ float4 average(const float4& acc, float sum) {
+  if (sum == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
+  return make_float4(acc.x / sum * kSumUp, acc.y / sum * kSumUp, acc.z / sum * kSumUp, acc.w / sum * kSumUp);
+}
 
 // Which part of which request a CTA of column `col` takes.  A part is up to W *
 // m groups, m the least number with which no more than a.columns parts come
@@ -623,8 +634,9 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
         join_sum(msum[j], sum[j], load_remote(mml + c, i), load_remote(ml + c, i));
       }
     }
-    // From units of 2^(M - 14) to the sum's.
-    if (mx > -INFINITY) scale4(acc[j], ex2(mx - kWeightLog2 - msum[j]));
+    // From units of 2^(M - 14) to the sum's (2^22 of them; a prefix's shares
+    // are joined in single ones).
+    if (mx > -INFINITY) scale4(acc[j], ex2(mx - kWeightLog2 - msum[j]) * (beside ? 1.f : kSumDown));
   }
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
@@ -639,10 +651,7 @@ __global__ void __launch_bounds__(W * 32, (kNT == 1 ? 12 : 8) / W)
     }
     const int s = (col0 + c) / a.G, gi = (col0 + c) % a.G;
     const int64_t at = ((static_cast<int64_t>(s) * a.R + r) * a.Hq + h * a.G + gi) * kHeadDim + lane * 4;
-    // What a query sees nothing of is 0.
-    const float4 v = sum[j] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                   : make_float4(acc[j].x / sum[j], acc[j].y / sum[j], acc[j].z / sum[j],
-                                                 acc[j].w / sum[j]);
+    const float4 v = average(acc[j], sum[j]);
     if (a.out_fp32) store4_finite(static_cast<float*>(a.out) + at, v);
     else store4_finite(static_cast<T*>(a.out) + at, v);
   }
@@ -742,9 +751,7 @@ __global__ void __launch_bounds__(128) join_parts(const Q8AttnArgs a) {
   float sum;
   const float4 acc = join_shares(reinterpret_cast<const float4*>(a.part) + at * 32, a.stat + at,
                                  static_cast<int64_t>(a.Hkv) * cols, parts, lane, sum);
-  // What a query sees nothing of is 0.
-  const float4 v = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : make_float4(acc.x / sum, acc.y / sum, acc.z / sum, acc.w / sum);
+  const float4 v = average(acc, sum);
   if (a.out_fp32) store4_finite(static_cast<float*>(a.out) + row * kHeadDim + lane * 4, v);
   else store4_finite(static_cast<T*>(a.out) + row * kHeadDim + lane * 4, v);
 }

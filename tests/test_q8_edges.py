@@ -89,3 +89,32 @@ def test_the_largest_values_come_back_finite(dev, dtype):  # noqa: F811
         near(got[0, 0, 0].view(1, -1), want[t:t + 1])
         assert (got[0, 1] == 0).all()
     assert c.oasis_q8_sync() == 0
+
+
+@pytest.mark.parametrize("lens,blocks", [([500, 33], 32), ([900], 512), ([700, 0, 3000], 1024)],
+                         ids=["one CTA", "cluster", "parts"])
+@pytest.mark.parametrize("S,G,fp32", [(1, 4, True), (4, 4, True), (2, 2, False)])
+def test_values_whose_sum_passes_the_range(dev, lens, blocks, S, G, fp32):  # noqa: F811
+    """Outputs are averages: values near the end of fp32's range give finite ones although their
+    sum is not."""
+    g = gen(71 + S)
+    c = ob.Q8Cache(ob.make_q8_config(sum(-(-n // 16) for n in lens), blocks, 2 * G, 2, out_fp32=fp32))
+    P = c.cfg.num_pages
+    k = torch.randn(P * 16, 2, 128, generator=g)
+    v = (2 * torch.rand(P * 16, 2, 128, generator=g) - 1) * (0.93 * 2.0 ** 127)
+    v[:, :, :8] = v[:1, :, :8]                            # the same in every token
+    c.oasis_q8_write(k.cuda(), v.cuda(), torch.arange(P * 16).cuda())
+    pages = c.pages.cpu().numpy()
+    table = Q.table_of(lens, P, blocks, g)
+    q = (0.5 * torch.randn(S, len(lens), 2 * G, 128, generator=g)).to(BF)
+    o, b = Q.attention(q, pages, table.numpy(), lens, True, out=FP if fp32 else BF)
+    assert np.abs(o).max() < 0.97 * 2.0 ** 127
+    t, m = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    out = torch.zeros(q.shape, dtype=FP if fp32 else BF, device=dev)
+    n = c.oasis_q8_attn_workspace(len(lens), S)
+    assert (n > 0) == (blocks == 1024)
+    for ws in ([torch.empty(n, dtype=torch.uint8, device=dev)] if n else []) + [torch.empty(0, dtype=torch.uint8, device=dev)]:
+        out.zero_()
+        c.oasis_q8_attn(q.cuda(), t, m, out, causal=True, workspace=ws)
+        close(out, o, b)
+    assert c.oasis_q8_sync() == 0
