@@ -17,6 +17,8 @@ using namespace oasis;
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int type_bytes(int type) { return type == OASIS_FP32 ? 4 : 2; }
 bool any_type(int type) { return type == OASIS_BF16 || type == OASIS_FP16 || type == OASIS_FP32; }
@@ -31,7 +33,8 @@ const char* config_error(const oasis_q8_config* c) {
   if (c->num_q_heads / c->num_kv_heads > kQ8MaxGroup) return "query heads per KV head must be <= 8";
   if (c->head_dim != kHeadDim) return "head_dim must be 128";
   if (c->block_size != kBlock) return "block_size must be 16";
-  if (!(c->softmax_scale >= 0.f) || std::isinf(c->softmax_scale)) return "softmax_scale must be finite and >= 0";
+  if (!(c->softmax_scale >= 0.f) || std::isinf(c->softmax_scale * kLog2e))
+    return "softmax_scale must be >= 0 and finite, also times log2(e)";
   if (c->out_fp32 != 0 && c->out_fp32 != 1) return "out_fp32 must be 0 or 1";
   if (c->device < 0) return "device must be >= 0";
   return nullptr;
@@ -111,7 +114,7 @@ OASIS_API int oasis_q8_init(const oasis_q8_config* cfg, void* pages, void* works
   q->cfg = *cfg;
   q->G = cfg->num_q_heads / cfg->num_kv_heads;
   const float scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.f / std::sqrt(static_cast<float>(kHeadDim));
-  q->scale_log2 = scale * 1.4426950408889634f;
+  q->scale_log2 = scale * kLog2e;
   q->pages = static_cast<uint8_t*>(pages);
   q->err = static_cast<uint32_t*>(workspace);
   *out = q;
