@@ -108,7 +108,7 @@ typedef struct {
   int32_t block_size;    /* B; must be 16 */
   int32_t topk;          /* K; 1..256 and K <= max_blocks */
   float fetch_ratio;     /* C = floor(fetch_ratio * K), 0 <= fetch_ratio <= 1 */
-  float softmax_scale;   /* 0 -> 1/sqrt(d); at most 2.35e38 */
+  float softmax_scale;   /* 0 -> 1/sqrt(d) */
   int32_t out_fp32;      /* attention outputs in fp32 (1) or bf16 (0) */
   int32_t device;        /* CUDA device ordinal */
   int32_t side_groups;   /* request groups oasis_step pipelines its side work
