@@ -612,9 +612,9 @@ OASIS_API int oasis_profile_read(oasis_ctx* ctx, double* ms_sum4,
  *          rounded to e4m3, ties to even, so a value is off by at most 2^-4
  *          of itself (and 2^(e - 10) near zero).  An infinity becomes the
  *          largest code (448) of its sign, NaN stays NaN.  A row's largest
- *          value may round to a power of two past its type's range (65504 to
- *          65536); where a call's output type ends below what codes stand for
- *          the output is that type's largest value, not an infinity.
+ *          value may round to the power of two past its type's range (in fp16
+ *          65504 to 65536, in bf16 and fp32 2^128): reads in that type, and
+ *          attention outputs, give the type's largest value for it.
  *   page_table  dev [R][max_blocks] int32: the page of each block.
  *   seq_len     dev [R] int32: tokens in the pages, <= 16 * max_blocks; a
  *          request with none (or fewer) is empty.  Entries of the table past
@@ -688,8 +688,8 @@ OASIS_API int oasis_q8_write(oasis_q8* q8, const void* k, const void* v, int typ
 
 /* Read R requests' tokens back: out dev [R][Hkv][out_blocks][2][B][d] of
  * `type`, the units of oasis_dense_attn's cache, of a host store and of
- * oasis_prefix_attn's prefix.  Exact in bf16 and fp32, rounded in fp16, and
- * in each held to the type's largest value.
+ * oasis_prefix_attn's prefix.  Exact in bf16 and fp32, rounded in fp16 (past
+ * its range, but for 65536, an infinity).
  * Tokens at or past seq_len (and those of a bad page) are left as they are.
  * out 16-byte aligned, out_blocks >= 1; a length past 16 * min(out_blocks,
  * max_blocks) raises BAD_BLOCK_ID and what fits is written. */

@@ -59,18 +59,25 @@ __device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d)
   return q8_pack2(a, b) | (q8_pack2(c, d) << 16);
 }
 
-// Two floats -> two of a 16-bit type, to nearest even; past its range the
-// largest of it, NaN stays NaN.  (What codes stand for is finite, but the
-// largest code a row's largest value rounds to can lie past the type's range.)
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two floats that codes stand for, or averages of them -> two of an output's
+// type, to nearest even, NaN as NaN.  A row's largest value may have the code of
+// the power of two past its type's range, 65536 or 2^128: that is given as the
+// type's largest value.  (Nothing else reaches 2^128; in fp16 what is larger
+// still, of a wider type, is an infinity as ever.)
 __device__ __forceinline__ uint32_t pack2_finite(const __nv_bfloat16*, float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 __device__ __forceinline__ uint32_t pack2_finite(const __half*, float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+  auto held = [](float x) {  // 65536, and 2^-11 of it for the rounding of sums
+    return fabsf(x) <= 65568.f ? fminf(fmaxf(x, -65504.f), 65504.f) : x;
+  };
+  return pack_f16x2(held(lo), held(hi));
 }
 __device__ __forceinline__ float finite(float x) {
   return fabsf(x) == INFINITY ? copysignf(__uint_as_float(0x7f7fffffu), x) : x;
@@ -88,10 +95,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // ---- launches that overlap (see launch_early)
@@ -169,7 +172,7 @@ __device__ __forceinline__ void store4(float* p, const float4& v) { *reinterpret
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
-// An output over codes, which is finite or NaN.
+// An output over codes.
 __device__ __forceinline__ void store4_finite(float* p, const float4& v) {
   store4(p, make_float4(finite(v.x), finite(v.y), finite(v.z), finite(v.w)));
 }

@@ -55,7 +55,7 @@ def test_pages_lent_at_any_multiple_of_sixteen_bytes(dev, dtype, off):  # noqa: 
 
 @pytest.mark.parametrize("dtype", [BF, HF, FP])
 def test_the_largest_values_come_back_finite(dev, dtype):  # noqa: F811
-    """A row's largest value can round up to a power of two past the type's range: it is read, and
+    """A row's largest value can round up to the power of two past the type's range: it is read, and
     attended to, as the type's largest value, within 2^-4 of what was written (half a step of e4m3;
     the type's own rounding of the output is less than the 2^-8 that the largest value is nearer)."""
     top = torch.finfo(dtype).max
@@ -76,10 +76,12 @@ def test_the_largest_values_come_back_finite(dev, dtype):  # noqa: F811
 
     def near(got, want):
         fin = torch.isfinite(want)
-        assert torch.isfinite(got[~torch.isnan(want)]).all() and torch.isnan(got[torch.isnan(want)]).all()
+        assert torch.isfinite(got[fin]).all() and torch.isnan(got[torch.isnan(want)]).all()
         assert ((got - want).abs()[fin] <= 2.0 ** -4 * want.abs()[fin]).all()
     near(back, want)
-    assert back[7, 3] > 0 > back[8, 3] and back[7, 3].abs() == top and back[8, 3].abs() == top
+    # infinities were written as the code of 448 * 2^e, past the type's range: 114688 in fp16
+    far = float("inf") if dtype == HF else top
+    assert back[7, 3] == far and back[8, 3] == -far
     # one token a request: its value is the output
     qt = HF if dtype == HF else BF
     for t in range(0, 32, 16):
@@ -118,3 +120,28 @@ def test_values_whose_sum_passes_the_range(dev, lens, blocks, S, G, fp32):  # no
         c.oasis_q8_attn(q.cuda(), t, m, out, causal=True, workspace=ws)
         close(out, o, b)
     assert c.oasis_q8_sync() == 0
+
+
+def test_fp16_rounds_wider_values_as_ever(dev):  # noqa: F811
+    """Values of a wider type past fp16's range are read, and attended to, as fp16 rounds them."""
+    x = torch.zeros(16, 1, 128)
+    x[0, 0, :8] = torch.tensor([1e6, -1e6, 65536.0, -65536.0, 73728.0, 3e38, 40000.0, 65504.0])
+    c = ob.Q8Cache(ob.make_q8_config(1, 1, 1, 1))
+    c.oasis_q8_write(torch.ones_like(x).cuda(), x.cuda(), torch.arange(16).cuda())
+    x[0, 0, 5] = 0
+    y = x.clone()
+    c2 = ob.Q8Cache(ob.make_q8_config(1, 1, 1, 1))
+    c2.oasis_q8_write(torch.ones_like(y).cuda(), y.cuda(), torch.arange(16).cuda())
+    for h in (c, c2):
+        t, m = torch.zeros(1, 1, dtype=torch.int32, device=dev), torch.ones(1, dtype=torch.int32, device=dev)
+        wide, half = (torch.zeros(1, 1, 1, 2, 16, 128, dtype=d, device=dev) for d in (FP, HF))
+        h.oasis_q8_read(t, m, wide)
+        h.oasis_q8_read(t, m, half)
+        v = wide[0, 0, 0, 1, 0].cpu()
+        want = torch.where(v.abs() == 65536, v.sign() * 65504, v).to(HF)
+        assert torch.equal(half[0, 0, 0, 1, 0].cpu(), want) and torch.isinf(want).any()
+        q = torch.ones(1, 1, 1, 128, dtype=HF, device=dev)
+        out = torch.zeros_like(q)
+        h.oasis_q8_attn(q, t, m, out)
+        assert torch.equal(out[0, 0, 0].cpu(), want)
+        assert h.oasis_q8_sync() == 0
