@@ -685,6 +685,10 @@ cudaError_t launch_t(const Q8AttnArgs& a, int col_groups, cudaStream_t s) {
   // queries 94, 71, 71, 87; 10 x 16 heads up to 20000 129, 96, 65, 72; but 32
   // even ones of 8192 89, 111, 98, 104.  Short contexts stay whole: 64 up to
   // 2000 33, 39, 45, 56.
+  // In rounds a request takes only as many of its cluster's CTAs as leave each
+  // of their warps `each` groups, six: 64 up to 8192 of which nine in ten have
+  // under 1024 tokens 60 us, with one group 64, with twelve 66 (all lengths
+  // alike, to 8192: 115, 115, 117).
   const int64_t slots = 152 * ((kNT == 1 ? 12 : 8) / W);
   const int64_t enough = kNT == 1 ? 3 * slots : slots * 3 / 2;
   int cluster = 1, each = 1;
@@ -781,8 +785,8 @@ cudaError_t launch_split(const Q8AttnArgs& a, int warps, cudaStream_t s) {
 // about one size fills the card, where a cluster ends at eight CTAs and keeps
 // the room of those that a short request leaves idle.  So: where the card holds
 // at least 1.7 CTAs a pair (of two warps with two column tiles), and in
-// clusters a warp of the longest request has
-// seven groups or more (of a single one, eight more than in parts).  GB300, us
+// clusters of one round a warp of the longest request has seven groups or more
+// (of a single one, eight more than in parts).  GB300, us
 // without and with (8 KV heads of four query heads, lengths uniform up to the
 // given one; in brackets four queries): 2 x 131072 118, 84 [157, 87]; 2 x 32000
 // 34, 25 [46, 32]; 5 x 30000 32, 27 [38, 35.5]; 24 x 9001 51.5, 49.5 [74, 61];
@@ -800,7 +804,9 @@ Q8Split q8_split(int R, int S, int G, int Hkv, int max_blocks) {
   const int64_t pairs = static_cast<int64_t>(R) * Hkv * col_groups;
   const int64_t groups = (max_blocks + kGroupUnits - 1) / kGroupUnits;
   const int64_t fit = 152 * CTAs;  // CTAs of four warps that the card holds
-  // Groups of a warp at the longest, in clusters (as launch_t takes them).
+  // Groups of a warp at the longest in clusters that fit the card at once: an
+  // estimate (launch_t goes on to more rounds of larger clusters, and to no
+  // more CTAs than there are groups), which the bounds below were measured with.
   int64_t cluster = 1;
   while (cluster < 8 && pairs * cluster * 2 <= fit) cluster *= 2;
   const int64_t whole = groups / (cluster * 4);

@@ -587,7 +587,8 @@ def oasis_q8_query_sizes(cfg: oasis_q8_config) -> oasis_q8_sizes:
 
 class Q8Cache:
     """A handle on an 8-bit paged KV cache: ``pages`` [num_pages][Hkv][4128]
-    uint8 (allocated zeroed unless passed in) and the handle's workspace.
+    uint8 (allocated zeroed unless passed in, 16-byte aligned; several handles
+    may have the same) and the handle's workspace.
     Methods map one-to-one onto the C ABI calls; tensors of another type,
     shape, device or layout than documented there are refused (ValueError).
     Calls run on ``stream`` (default: the device's current one); tensors

@@ -122,6 +122,31 @@ def test_values_whose_sum_passes_the_range(dev, lens, blocks, S, G, fp32):  # no
     assert c.oasis_q8_sync() == 0
 
 
+def test_handles_on_the_same_pages_with_tables_of_other_widths(dev):  # noqa: F811
+    """A second handle with fewer blocks a row, on the same pages: each writes what the other reads,
+    and both attend within the bound over tables of their own width."""
+    g = gen(91)
+    lens = [100, 33, 0, 160]
+    wide = ob.Q8Cache(ob.make_q8_config(40, 4096, 16, 4, out_fp32=True))
+    narrow = ob.Q8Cache(ob.make_q8_config(40, 10, 16, 4, out_fp32=True), pages=wide.pages)
+    k, v = torch.randn(2, 640, 4, 128, generator=g)
+    wide.oasis_q8_write(k[:300].cuda(), v[:300].cuda(), torch.arange(300).cuda())
+    narrow.oasis_q8_write(k[300:].cuda(), v[300:].cuda(), torch.arange(300, 640).cuda())
+    t = Q.table_of(lens, 40, 10, g)
+    t_wide = torch.full((4, 4096), -1, dtype=torch.int32)
+    t_wide[:, :10] = t
+    q = torch.randn(2, 4, 16, 128, generator=g).to(BF)
+    o, b = Q.attention(q, wide.pages.cpu().numpy(), t.numpy(), lens, True, out=FP)
+    close(attend(wide, q.cuda(), t_wide, lens, True), o, b)
+    close(attend(narrow, q.cuda(), t, lens, True), o, b)
+    m = torch.tensor(lens, dtype=torch.int32).cuda()
+    a, c = (torch.zeros(4, 4, 10, 2, 16, 128, dtype=BF, device=dev) for _ in range(2))
+    wide.oasis_q8_read(t_wide.cuda(), m, a)
+    narrow.oasis_q8_read(t.cuda(), m, c)
+    assert wide.oasis_q8_sync() == 0 and narrow.oasis_q8_sync() == 0
+    assert torch.equal(a, c)
+
+
 def test_fp16_rounds_wider_values_as_ever(dev):  # noqa: F811
     """Values of a wider type past fp16's range are read, and attended to, as fp16 rounds them."""
     x = torch.zeros(16, 1, 128)
