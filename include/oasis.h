@@ -789,6 +789,111 @@ typedef struct {
 OASIS_API const char* oasis_verify_error(const oasis_verify_args* args);
 OASIS_API int oasis_verify_drafts(const oasis_verify_args* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens over the 8-bit cache.  One step of a request: its
+ * nodes' keys and values are turned by their positions and appended behind
+ * the context, every node attends to the context and to the nodes that it
+ * follows, the logits' log probabilities say which nodes stay, and those are
+ * moved to the tree's first places.  The same rules of streams, capture and
+ * device error bits as above.
+ * ------------------------------------------------------------------------ */
+
+/* Rotation by position: of pair i < rot_dim / 2 of a head's first rot_dim
+ * dims, (a, b) becomes scale * (a cos w - b sin w, a sin w + b cos w) with
+ * w = position[axis[i]] * frequency[i].  The other dims stay. */
+typedef struct {
+  int32_t rot_dim;      /* a multiple of 16, 16..128 */
+  int32_t num_axes;     /* rows of positions, 1..4 (time, height, width, ..) */
+  int32_t interleaved;  /* pair i: dims 2 i, 2 i + 1 (1) or i, i + rot_dim / 2 (0) */
+  float scale;          /* 0 -> 1; finite, >= 0 */
+  double frequency[64]; /* radians a position, magnitudes up to 2^20 */
+  int32_t axis[64];     /* of each pair, 0..num_axes - 1 */
+} oasis_rope;
+
+/* NULL if the rotation is supported, else a static message naming the first
+ * problem.  Pure host computation. */
+OASIS_API const char* oasis_rope_error(const oasis_rope* rope);
+
+/* oasis_q8_write of T tokens whose keys, and queries, are turned first.
+ * q [T][Hq][d], k, v [T][Hkv][d] of `type`, consecutive tokens *_stride
+ * elements apart, 16-byte aligned as the strides' bytes; q_out of `type`
+ * likewise; it may be q itself (with its stride), but not overlap the inputs
+ * in another way.  q and q_out may be NULL (keys alone).  positions: dev
+ * [num_axes][T] int64, any values.  Tokens with a negative slot are not
+ * written; their queries are turned all the same.
+ * Precision: an angle's error does not grow with its position (2^-23 of a
+ * turn); turning is fp32, rounded once, to q_out's type and to codes: keys are
+ * not rounded to `type` between.  A row whose largest value comes within
+ * fp32's rounding of a border of two exponents may get either.  The values are
+ * oasis_q8_write's. */
+OASIS_API int oasis_q8_append(oasis_q8* q8, const oasis_rope* rope, const void* q, void* q_out,
+                              const void* k, const void* v, int type, int64_t q_stride,
+                              int64_t q_out_stride, int64_t k_stride, int64_t v_stride,
+                              const int64_t* positions, const int64_t* slots, int num_tokens,
+                              void* stream);
+
+/* Attention of up to N = num_nodes (1..64) drafted nodes a request.  The last
+ * n_r tokens of request r (n_r = tree_size[r], held to 0..N, or N where
+ * tree_size is NULL) are its nodes: node i is token seq_len[r] - n_r + i.
+ * Every node sees the tokens before the first node, and node j where bit j of
+ * tree[r][i] is set (itself too; bits from n_r on do not count).  q, out: dev
+ * [R][N][Hq][d], 16-byte aligned, not overlapping; q of `type` (OASIS_BF16 or
+ * _FP16), out of that type, or fp32 with cfg.out_fp32.  tree: dev [R][N]
+ * uint64.  Rows of out from n_r on are left as they are.  A node that sees
+ * nothing, and those of a request with no tokens, give zeros; so do those of a
+ * request with fewer tokens than nodes, which raises BAD_BLOCK_ID.
+ * num_requests <= 65535, R * N * Hq < 2^31. */
+OASIS_API int oasis_q8_tree_attn(oasis_q8* q8, int num_requests, int num_nodes, const void* q, int type,
+                                 const uint64_t* tree, const int32_t* tree_size,
+                                 const int32_t* page_table, const int32_t* seq_len, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+/* Scratch that oasis_q8_tree_attn wants for these sizes (device memory,
+ * 256-byte aligned; 0 is possible).  A call's scratch must not be given to
+ * another that may run at the same time. */
+OASIS_API int oasis_q8_tree_workspace(const oasis_q8* q8, int num_requests, int num_nodes, size_t* bytes);
+
+/* Keep some nodes of each request's tree: for i < keep[r] the keys and values
+ * of node nodes[r][i] move to node i's place (codes and exponents as they are;
+ * of a request, all are read before any is written, so its lists may be in
+ * any order and name a node twice).  nodes: dev [R][M] int32, keep: dev [R]
+ * int32, held to 0..min(M, n_r); num_nodes, tree_size and seq_len as above
+ * (before they are lowered).  A node outside 0..n_r - 1 raises BAD_UNIT and its
+ * place stays as it is; a bad page or a length under n_r BAD_BLOCK_ID.
+ * max_keep = M, 1..64.  A page must not be in two requests' trees. */
+OASIS_API int oasis_q8_keep(oasis_q8* q8, int num_requests, int num_nodes, const int32_t* tree_size,
+                            const int32_t* page_table, const int32_t* seq_len, const int32_t* nodes,
+                            const int32_t* keep, int max_keep, void* stream);
+
+/* Log probabilities under softmax(x) of each row x of logits, in nats:
+ *   logprobs[r]  of token tokens[r] (-infinity for one >= V);
+ *   entropy[r]   -sum p log p;
+ *   top_ids[r][j], top_logprobs[r][j]  of the j-th largest entry, j < top, of
+ *                equal ones the lower token first (-1, -infinity past V).
+ * A row with tokens[r] < 0 is not wanted: it is not read and its outputs are
+ * left as they are.  Entries of -infinity have probability 0.  Rows with NaN
+ * or +infinity, or nothing above -infinity, give NaN (of the first kinds ids
+ * are unspecified).  Sums are fp32: a value is off by at most 2^-19 + 2^-21 of
+ * itself and 2^-22 (x_max - x) for a token's x. */
+typedef struct {
+  int32_t num_rows;       /* 0..2^24 */
+  int32_t vocab;          /* V, 1..2^20 */
+  int32_t type;           /* of the logits: OASIS_BF16, _FP16, _FP32 */
+  int32_t top;            /* alternatives, 0..32 */
+  int32_t device;         /* CUDA device ordinal */
+  const void* logits;     /* dev rows of V, stride elements apart; aligned to their type */
+  int64_t stride;         /* >= V */
+  const int32_t* tokens;  /* dev [num_rows], or NULL: no given tokens, all rows wanted */
+  float* logprobs;        /* dev [num_rows]; NULL: not wanted, as where tokens is NULL */
+  float* entropy;         /* dev [num_rows], or NULL */
+  int32_t* top_ids;       /* dev [num_rows][top]; NULL with top = 0 */
+  float* top_logprobs;    /* dev [num_rows][top] */
+} oasis_logprobs_args;
+
+/* NULL if the call is supported, else a static message naming the first
+ * problem.  Pure host computation. */
+OASIS_API const char* oasis_logprobs_error(const oasis_logprobs_args* args);
+OASIS_API int oasis_token_logprobs(const oasis_logprobs_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

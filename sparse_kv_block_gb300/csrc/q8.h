@@ -13,6 +13,8 @@ enum Q8Type { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
 constexpr int kQ8MaxGroup = 8;     // query heads per KV head
 constexpr int kQ8MaxQueries = 4;   // queries per request
 constexpr int kVerifyMaxDrafts = 64;
+constexpr int kTreeMaxNodes = 64;  // bits of a node's word
+constexpr int kLogprobsMaxTop = 32;
 
 struct Q8WriteArgs {
   const void* k;             // [T][Hkv][d], token stride in elements
@@ -23,6 +25,57 @@ struct Q8WriteArgs {
   uint32_t* err;
   int64_t num_slots;         // num_pages * 16
   int T, Hkv, type;
+};
+
+struct AppendArgs {
+  Q8WriteArgs kv;            // keys (to be turned), values and where they go
+  const void* q;             // [T][Hq][d], token stride in elements
+  void* out;                 // turned queries
+  int64_t q_stride, out_stride;
+  const int64_t* positions;  // [axes][T]
+  int Hq;                    // 0: keys alone
+  int half, interleaved;     // pairs; (2 i, 2 i + 1) in place of (i, i + half)
+  float scale;               // of cos and sin
+  int chunk, chunks;         // heads of a warp (the launcher's)
+  uint64_t turn[64];         // of a pair: turns a position, in units of 2^-64
+  uint8_t axis[64];
+};
+
+struct KeepArgs {
+  uint8_t* pages;
+  const int32_t* table;      // [R][max_blocks]
+  const int32_t* len;        // [R], the tree's nodes included
+  const int32_t* size;       // [R] or null: N
+  const int32_t* nodes;      // [R][M]
+  const int32_t* keep;       // [R]
+  uint32_t* err;
+  int R, N, M, Hkv, num_pages, max_blocks;
+};
+
+struct TreeArgs {
+  const void* q;             // [R][N][Hq][d]
+  void* out;
+  const uint8_t* pages;
+  const uint64_t* words;     // [R][N]: bit j of node i's: it sees node j
+  const int32_t* table;      // [R][max_blocks]
+  const int32_t* len;        // [R], the tree's nodes included
+  const int32_t* size;       // [R] or null: N
+  uint32_t* err;
+  int R, N, Hq, Hkv, G, num_pages, max_blocks;
+  int type, out_fp32;
+  float scale_log2;
+  long long wait_limit;
+};
+
+struct LogprobsArgs {
+  const void* logits;        // rows of V, stride elements apart
+  int64_t stride;
+  const int32_t* tokens;     // [rows] or null
+  float* logprobs;           // [rows] or null
+  float* entropy;            // [rows] or null
+  int32_t* top_ids;          // [rows][k]
+  float* top_logprobs;
+  int rows, V, k, type;
 };
 
 struct Q8ReadArgs {
@@ -132,11 +185,18 @@ PrefixShape prefix_shape(int R, int S, int G, int Hkv, int prefix_len);
 cudaError_t launch_prefix(const PrefixArgs& a, int tiles, const CUtensorMap& map, cudaStream_t s);
 cudaError_t launch_join(const PrefixArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
+cudaError_t launch_q8_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_q8_keep(const KeepArgs& a, cudaStream_t s);
+cudaError_t launch_q8_tree(const TreeArgs& a, cudaStream_t s);
+cudaError_t launch_logprobs(const LogprobsArgs& a, cudaStream_t s);
 
 // Load the kernels' code (and set their shared memory) on the current device.
 cudaError_t preload_q8_cache_kernels();
 cudaError_t preload_q8_attn_kernels();
 cudaError_t preload_prefix_kernels();
 cudaError_t preload_verify_kernels();
+cudaError_t preload_append_kernels();
+cudaError_t preload_tree_kernels();
+cudaError_t preload_logprobs_kernels();
 
 }  // namespace oasis

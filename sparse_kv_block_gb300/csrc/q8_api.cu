@@ -103,7 +103,8 @@ OASIS_API int oasis_q8_init(const oasis_q8_config* cfg, void* pages, void* works
   OnDevice dev(cfg->device);
   if (dev.error() != cudaSuccess) return OASIS_ECUDA;
   if (preload_q8_cache_kernels() != cudaSuccess || preload_q8_attn_kernels() != cudaSuccess ||
-      preload_prefix_kernels() != cudaSuccess)
+      preload_prefix_kernels() != cudaSuccess || preload_append_kernels() != cudaSuccess ||
+      preload_tree_kernels() != cudaSuccess)
     return OASIS_ECUDA;
   // The caller's memory may still be written by what it was used for before.
   if (cudaDeviceSynchronize() != cudaSuccess) return OASIS_ECUDA;
@@ -430,4 +431,216 @@ OASIS_API int oasis_verify_drafts(const oasis_verify_args* a, void* stream) {
     loaded.fetch_or(bit, std::memory_order_release);
   }
   return launch_verify(v, static_cast<cudaStream_t>(stream)) == cudaSuccess ? OASIS_OK : OASIS_ECUDA;
+}
+
+OASIS_API const char* oasis_rope_error(const oasis_rope* r) {
+  if (!r) return "null rotation";
+  if (r->rot_dim < 16 || r->rot_dim > kHeadDim || r->rot_dim % 16 != 0)
+    return "rot_dim must be a multiple of 16 in 16..128";
+  if (r->num_axes < 1 || r->num_axes > 4) return "num_axes must be in 1..4";
+  if (r->interleaved != 0 && r->interleaved != 1) return "interleaved must be 0 or 1";
+  if (!(r->scale >= 0.f) || std::isinf(r->scale)) return "scale must be >= 0 and finite";
+  for (int i = 0; i < r->rot_dim / 2; ++i) {
+    if (!(std::fabs(r->frequency[i]) <= 0x1p20)) return "frequencies must be finite, up to 2^20";
+    if (r->axis[i] < 0 || r->axis[i] >= r->num_axes) return "axis must be in 0..num_axes - 1";
+  }
+  return nullptr;
+}
+
+namespace {
+
+// A frequency in radians as turns modulo one, in units of 2^-64: the product
+// with 1 / (2 pi), given in two doubles, to about 2^-100 of itself.
+uint64_t turns(double radians) {
+  constexpr double kInv = 0x1.45f306dc9c883p-3, kInvLow = -0x1.6b01ec5417056p-57;
+  const double r = std::fabs(radians), hi = r * kInv;
+  const double lo = std::fma(r, kInv, -hi) + r * kInvLow;
+  const uint64_t u = static_cast<uint64_t>(std::ldexp(hi - std::floor(hi), 64)) +
+                     static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(std::ldexp(lo, 64))));
+  return radians < 0 ? 0 - u : u;
+}
+
+}  // namespace
+
+OASIS_API int oasis_q8_append(oasis_q8* q8, const oasis_rope* rope, const void* q, void* q_out,
+                              const void* k, const void* v, int type, int64_t q_stride,
+                              int64_t q_out_stride, int64_t k_stride, int64_t v_stride,
+                              const int64_t* positions, const int64_t* slots, int num_tokens,
+                              void* stream) {
+  if (!q8) return OASIS_EINVAL;
+  if (const char* m = oasis_rope_error(rope)) return q8->fail(OASIS_EINVAL, "q8_append: %s", m);
+  if (!any_type(type)) return q8->fail(OASIS_EINVAL, "q8_append: bad type %d", type);
+  if (num_tokens < 0) return q8->fail(OASIS_EINVAL, "q8_append: num_tokens must be >= 0");
+  if (static_cast<int64_t>(num_tokens) * (q8->cfg.num_q_heads + q8->cfg.num_kv_heads) > (1ll << 32))
+    return q8->fail(OASIS_EINVAL, "q8_append: num_tokens * (query + KV heads) must be <= 2^32");
+  if (num_tokens == 0) return OASIS_OK;
+  if (!k || !v || !positions || !slots || !q != !q_out) return q8->fail(OASIS_EINVAL, "q8_append: null pointer");
+  const int b = type_bytes(type);
+  auto fits = [&](const void* p, int64_t stride) { return aligned(p, 16) && stride >= 0 && stride * b % 16 == 0; };
+  if (!fits(k, k_stride) || !fits(v, v_stride) || !aligned(positions, 8) || !aligned(slots, 8) ||
+      (q && (!fits(q, q_stride) || !fits(q_out, q_out_stride))))
+    return q8->fail(OASIS_EINVAL, "q8_append: q, q_out, k, v and their strides must be 16-byte aligned, the strides >= 0");
+  if (q && num_tokens > 1 && q_out_stride < static_cast<int64_t>(q8->cfg.num_q_heads) * kHeadDim)
+    return q8->fail(OASIS_EINVAL, "q8_append: q_out_stride must be at least a token's queries");
+  OnDevice dev(q8->cfg.device);
+  if (int rc = q8->cuda(dev.error(), "cudaSetDevice")) return rc;
+  AppendArgs a{};
+  a.kv.k = k;
+  a.kv.v = v;
+  a.kv.k_stride = k_stride;
+  a.kv.v_stride = v_stride;
+  a.kv.slots = slots;
+  a.kv.pages = q8->pages;
+  a.kv.err = q8->err;
+  a.kv.num_slots = static_cast<int64_t>(q8->cfg.num_pages) * kBlock;
+  a.kv.T = num_tokens;
+  a.kv.Hkv = q8->cfg.num_kv_heads;
+  a.kv.type = type;
+  a.q = q;
+  a.out = q_out;
+  a.q_stride = q_stride;
+  a.out_stride = q_out_stride;
+  a.positions = positions;
+  a.Hq = q ? q8->cfg.num_q_heads : 0;
+  a.half = rope->rot_dim / 2;
+  a.interleaved = rope->interleaved;
+  a.scale = rope->scale > 0.f ? rope->scale : 1.f;
+  for (int i = 0; i < a.half; ++i) {
+    a.turn[i] = turns(rope->frequency[i]);
+    a.axis[i] = static_cast<uint8_t>(rope->axis[i]);
+  }
+  return q8->cuda(launch_q8_append(a, static_cast<cudaStream_t>(stream)), "q8_append launch");
+}
+
+OASIS_API int oasis_q8_tree_workspace(const oasis_q8* q8, int num_requests, int num_nodes, size_t* bytes) {
+  if (!q8 || !bytes || num_requests < 0 || num_requests > 65535 || num_nodes < 1 || num_nodes > kTreeMaxNodes)
+    return OASIS_EINVAL;
+  *bytes = 0;
+  return OASIS_OK;
+}
+
+OASIS_API int oasis_q8_tree_attn(oasis_q8* q8, int num_requests, int num_nodes, const void* q, int type,
+                                 const uint64_t* tree, const int32_t* tree_size,
+                                 const int32_t* page_table, const int32_t* seq_len, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q8) return OASIS_EINVAL;
+  if (type != OASIS_BF16 && type != OASIS_FP16)
+    return q8->fail(OASIS_EINVAL, "q8_tree_attn: queries must be bf16 or fp16");
+  if (num_requests < 0 || num_requests > 65535)
+    return q8->fail(OASIS_EINVAL, "q8_tree_attn: num_requests must be in 0..65535");
+  if (num_nodes < 1 || num_nodes > kTreeMaxNodes)
+    return q8->fail(OASIS_EINVAL, "q8_tree_attn: num_nodes must be in 1..64");
+  if (static_cast<int64_t>(num_requests) * num_nodes * q8->cfg.num_q_heads > 0x7fffffff)
+    return q8->fail(OASIS_EINVAL, "q8_tree_attn: too many query vectors");
+  if (num_requests == 0) return OASIS_OK;
+  if (!q || !out || !tree || !page_table || !seq_len) return q8->fail(OASIS_EINVAL, "q8_tree_attn: null pointer");
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(tree, 8) || !aligned(tree_size, 4) ||
+      !aligned(page_table, 4) || !aligned(seq_len, 4))
+    return q8->fail(OASIS_EINVAL, "q8_tree_attn: misaligned pointer (q, out: 16 bytes, tree: 8)");
+  size_t need = 0;
+  oasis_q8_tree_workspace(q8, num_requests, num_nodes, &need);
+  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    return q8->fail(OASIS_EINVAL, "q8_tree_attn: workspace null, misaligned (256 bytes) or under %zu bytes", need);
+  OnDevice dev(q8->cfg.device);
+  if (int rc = q8->cuda(dev.error(), "cudaSetDevice")) return rc;
+  TreeArgs a{};
+  a.q = q;
+  a.out = out;
+  a.pages = q8->pages;
+  a.words = tree;
+  a.table = page_table;
+  a.len = seq_len;
+  a.size = tree_size;
+  a.err = q8->err;
+  a.R = num_requests;
+  a.N = num_nodes;
+  a.Hq = q8->cfg.num_q_heads;
+  a.Hkv = q8->cfg.num_kv_heads;
+  a.G = q8->G;
+  a.num_pages = q8->cfg.num_pages;
+  a.max_blocks = q8->cfg.max_blocks;
+  a.type = type;
+  a.out_fp32 = q8->cfg.out_fp32;
+  a.scale_log2 = q8->scale_log2;
+  a.wait_limit = q8->wait_limit;
+  return q8->cuda(launch_q8_tree(a, static_cast<cudaStream_t>(stream)), "q8_tree_attn launch");
+}
+
+OASIS_API int oasis_q8_keep(oasis_q8* q8, int num_requests, int num_nodes, const int32_t* tree_size,
+                            const int32_t* page_table, const int32_t* seq_len, const int32_t* nodes,
+                            const int32_t* keep, int max_keep, void* stream) {
+  if (!q8) return OASIS_EINVAL;
+  if (num_requests < 0 || num_requests > 65535)
+    return q8->fail(OASIS_EINVAL, "q8_keep: num_requests must be in 0..65535");
+  if (num_nodes < 1 || num_nodes > kTreeMaxNodes || max_keep < 1 || max_keep > kTreeMaxNodes)
+    return q8->fail(OASIS_EINVAL, "q8_keep: num_nodes and max_keep must be in 1..64");
+  if (static_cast<int64_t>(num_requests) * q8->cfg.num_kv_heads > 0x7fffffff)
+    return q8->fail(OASIS_EINVAL, "q8_keep: num_requests * num_kv_heads must be < 2^31");
+  if (num_requests == 0) return OASIS_OK;
+  if (!page_table || !seq_len || !nodes || !keep) return q8->fail(OASIS_EINVAL, "q8_keep: null pointer");
+  if (!aligned(tree_size, 4) || !aligned(page_table, 4) || !aligned(seq_len, 4) || !aligned(nodes, 4) ||
+      !aligned(keep, 4))
+    return q8->fail(OASIS_EINVAL, "q8_keep: misaligned pointer");
+  OnDevice dev(q8->cfg.device);
+  if (int rc = q8->cuda(dev.error(), "cudaSetDevice")) return rc;
+  KeepArgs a{};
+  a.pages = q8->pages;
+  a.table = page_table;
+  a.len = seq_len;
+  a.size = tree_size;
+  a.nodes = nodes;
+  a.keep = keep;
+  a.err = q8->err;
+  a.R = num_requests;
+  a.N = num_nodes;
+  a.M = max_keep;
+  a.Hkv = q8->cfg.num_kv_heads;
+  a.num_pages = q8->cfg.num_pages;
+  a.max_blocks = q8->cfg.max_blocks;
+  return q8->cuda(launch_q8_keep(a, static_cast<cudaStream_t>(stream)), "q8_keep launch");
+}
+
+OASIS_API const char* oasis_logprobs_error(const oasis_logprobs_args* a) {
+  if (!a) return "null arguments";
+  if (a->num_rows < 0 || a->num_rows > (1 << 24)) return "num_rows must be in 0..2^24";
+  if (a->vocab < 1 || a->vocab > (1 << 20)) return "vocab must be in 1..2^20";
+  if (!any_type(a->type)) return "type must be OASIS_BF16, OASIS_FP16 or OASIS_FP32";
+  if (a->top < 0 || a->top > kLogprobsMaxTop) return "top must be in 0..32";
+  if (a->device < 0) return "device must be >= 0";
+  if (a->num_rows == 0) return nullptr;
+  if (!a->logits) return "null pointer (logits)";
+  if (a->top > 0 && (!a->top_ids || !a->top_logprobs)) return "null pointer (top_ids or top_logprobs)";
+  if (a->logprobs && !a->tokens) return "logprobs without tokens";
+  if (a->stride < a->vocab) return "stride must be >= vocab";
+  if (!aligned(a->logits, type_bytes(a->type)) || !aligned(a->tokens, 4) || !aligned(a->logprobs, 4) ||
+      !aligned(a->entropy, 4) || !aligned(a->top_ids, 4) || !aligned(a->top_logprobs, 4))
+    return "a pointer is not aligned to its type";
+  return nullptr;
+}
+
+OASIS_API int oasis_token_logprobs(const oasis_logprobs_args* a, void* stream) {
+  if (oasis_logprobs_error(a)) return OASIS_EINVAL;
+  if (a->num_rows == 0) return OASIS_OK;
+  OnDevice dev(a->device);
+  if (dev.error() != cudaSuccess) return OASIS_ECUDA;
+  LogprobsArgs l{};
+  l.logits = a->logits;
+  l.stride = a->stride;
+  l.tokens = a->tokens;
+  l.logprobs = a->logprobs;
+  l.entropy = a->entropy;
+  l.top_ids = a->top_ids;
+  l.top_logprobs = a->top_logprobs;
+  l.rows = a->num_rows;
+  l.V = a->vocab;
+  l.k = a->top;
+  l.type = a->type;
+  // (As oasis_verify_drafts.)
+  static std::atomic<uint64_t> loaded{0};
+  const uint64_t bit = a->device < 64 ? 1ull << a->device : 0;
+  if (!(loaded.load(std::memory_order_acquire) & bit)) {
+    if (preload_logprobs_kernels() != cudaSuccess) return OASIS_ECUDA;
+    loaded.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_logprobs(l, static_cast<cudaStream_t>(stream)) == cudaSuccess ? OASIS_OK : OASIS_ECUDA;
 }

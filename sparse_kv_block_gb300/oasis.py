@@ -78,6 +78,20 @@ class oasis_verify_args(ctypes.Structure):
                 ("u_sample", c_void_p), ("out_tokens", c_void_p), ("n_accept", c_void_p)]
 
 
+class oasis_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", c_int32), ("num_axes", c_int32), ("interleaved", c_int32),
+                ("scale", c_float), ("frequency", c_double * 64), ("axis", c_int32 * 64)]
+
+
+class oasis_logprobs_args(ctypes.Structure):
+    _fields_ = [("num_rows", c_int32), ("vocab", c_int32), ("type", c_int32), ("top", c_int32),
+                ("device", c_int32), ("logits", c_void_p), ("stride", c_int64),
+                ("tokens", c_void_p), ("logprobs", c_void_p), ("entropy", c_void_p),
+                ("top_ids", c_void_p), ("top_logprobs", c_void_p)]
+
+
+_LOGPROBS_ARGS = struct.Struct("@5iPqPPPPP")
+assert _LOGPROBS_ARGS.size == ctypes.sizeof(oasis_logprobs_args)
 _VERIFY_ARGS = struct.Struct("@5iPPqqPPPPPP")
 assert _VERIFY_ARGS.size == ctypes.sizeof(oasis_verify_args)
 
@@ -158,6 +172,14 @@ EXPORTS = {
                                   _P, _P, c_size_t, _P]),
     "oasis_verify_error": (c_char_p, [_P]),
     "oasis_verify_drafts": (c_int, [_P, _P]),
+    "oasis_rope_error": (c_char_p, [POINTER(oasis_rope)]),
+    "oasis_q8_append": (c_int, [_P, POINTER(oasis_rope), _P, _P, _P, _P, c_int, c_int64, c_int64,
+                                c_int64, c_int64, _P, _P, c_int, _P]),
+    "oasis_q8_tree_attn": (c_int, [_P, c_int, c_int, _P, c_int, _P, _P, _P, _P, _P, _P, c_size_t, _P]),
+    "oasis_q8_tree_workspace": (c_int, [_P, c_int, c_int, POINTER(c_size_t)]),
+    "oasis_q8_keep": (c_int, [_P, c_int, c_int, _P, _P, _P, _P, _P, c_int, _P]),
+    "oasis_logprobs_error": (c_char_p, [_P]),
+    "oasis_token_logprobs": (c_int, [_P, _P]),
 }
 
 PROFILE_KINDS = ["attention", "score_topk", "admit_evict", "prefetch", "demand_score",
@@ -585,6 +607,45 @@ def oasis_q8_query_sizes(cfg: oasis_q8_config) -> oasis_q8_sizes:
     return out
 
 
+def make_rope(rot_dim=128, base=10000.0, sections=None, frequency=None, axis=None, interleaved=False,
+              scale=1.0) -> oasis_rope:
+    """A rotation by position.  ``frequency``: radians a position of each of the rot_dim / 2 pairs
+    (default base^(-2 i / rot_dim)).  Several position axes (time, height, width): ``sections``,
+    the pairs of each axis in order, or ``axis``, each pair's axis."""
+    half = rot_dim // 2
+    if frequency is None:
+        frequency = [float(base) ** (-2.0 * i / rot_dim) for i in range(half)]
+    if sections is not None:
+        if axis is not None:
+            raise ValueError("sections or axis, not both")
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    axis = [0] * half if axis is None else [int(a) for a in axis]
+    if len(frequency) != half or len(axis) != half or half > 64:
+        raise ValueError(f"a rotation of {rot_dim} dims has {half} pairs (at most 64): got {len(frequency)} "
+                         f"frequencies and {len(axis)} axes")
+    r = oasis_rope(rot_dim, max(axis, default=0) + 1, 1 if interleaved else 0, scale)
+    r.frequency[:half] = [float(f) for f in frequency]
+    r.axis[:half] = axis
+    m = lib().oasis_rope_error(ctypes.byref(r))
+    if m is not None:
+        raise OasisError(OASIS_EINVAL, m.decode())
+    return r
+
+
+def tree_words(parents) -> torch.Tensor:
+    """The words of oasis_q8_tree_attn, int64 like parents, of trees given by their nodes' parents
+    [..., N] (before the node; negative: the context): a node sees its ancestors and itself."""
+    p = torch.as_tensor(parents).cpu().long()
+    N = p.shape[-1]
+    if N > 64 or (p >= torch.arange(N)).any():
+        raise ValueError("a tree has up to 64 nodes, and a node's parent stands before it")
+    w = torch.zeros(*p.shape[:-1], N + 1, dtype=torch.int64)  # the last: the context's
+    for i in range(N):
+        up = torch.where(p[..., i] < 0, N, p[..., i]).unsqueeze(-1)
+        w[..., i] = w.gather(-1, up).squeeze(-1) | (-(1 << 63) if i == 63 else 1 << i)
+    return w[..., :N].contiguous()
+
+
 class Q8Cache:
     """A handle on an 8-bit paged KV cache: ``pages`` [num_pages][Hkv][4128]
     uint8 (allocated zeroed unless passed in, 16-byte aligned; several handles
@@ -752,6 +813,124 @@ class Q8Cache:
         self._check(self._lib.oasis_prefix_attn(self.q8, R, S, 1 if causal else 0, qp, typ, kv, blocks,
                                                 prefix_len, table, lens, o, ws, n,
                                                 _stream_on(stream, self._dev)))
+
+
+    def _tokens(self, name: str, x: torch.Tensor, T: int, H: int, dtype) -> tuple:
+        """The address of x [T][H][d], whose heads are contiguous, and its elements a token."""
+        if x.dtype is not dtype or x.shape != (T, H, 128) or x.get_device() != self._dev:
+            raise ValueError(f"{name} must be {dtype} {[T, H, 128]} on {self.device}, got {x.dtype} "
+                             f"{list(x.shape)} on {x.device}")
+        st = x.stride()
+        if T and (st[2] != 1 or (H > 1 and st[1] != 128)):
+            raise ValueError(f"{name}: a token's heads must be contiguous")
+        return x.data_ptr(), st[0] if T > 1 else H * 128
+
+    def oasis_q8_append(self, rope: oasis_rope, q, k, v, positions, slots, q_out, stream=None) -> None:
+        """q, q_out [T][Hq][128] (or both None), k, v [T][Hkv][128] bf16, fp16 or fp32 (tokens may
+        be strided; q_out may be q), positions [axes][T] (or [T]) and slots [T] int64; rope from
+        make_rope."""
+        T = slots.numel()
+        typ = _TYPES.get(k.dtype)
+        if typ is None:
+            raise ValueError(f"k must be bfloat16, float16 or float32, got {k.dtype}")
+        kp, ks = self._tokens("k", k, T, self._Hkv, k.dtype)
+        vp, vs = self._tokens("v", v, T, self._Hkv, k.dtype)
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out come together")
+        qp, qs = (None, 0) if q is None else self._tokens("q", q, T, self._Hq, k.dtype)
+        op, os_ = (None, 0) if q is None else self._tokens("q_out", q_out, T, self._Hq, k.dtype)
+        shape = (rope.num_axes, T) if rope.num_axes > 1 or positions.dim() != 1 else (T,)
+        self._check(self._lib.oasis_q8_append(
+            self.q8, ctypes.byref(rope), qp, op, kp, vp, typ, qs, os_, ks, vs,
+            _want("positions", positions, torch.int64, shape, self._dev),
+            _want("slots", slots, torch.int64, (T,), self._dev), T, _stream_on(stream, self._dev)))
+
+    def oasis_q8_tree_workspace(self, R: int, N: int) -> int:
+        n = c_size_t(0)
+        rc = lib().oasis_q8_tree_workspace(self.q8, R, N, ctypes.byref(n))
+        if rc != OASIS_OK:
+            raise OasisError(rc, "q8_tree_workspace: bad size")
+        return n.value
+
+    def oasis_q8_tree_attn(self, q, tree, page_table, seq_len, out, tree_size=None, stream=None,
+                           workspace=None) -> None:
+        """q, out [R][N][Hq][128], tree [R][N] int64 (see tree_words), tree_size [R] int32.
+        workspace: scratch of oasis_q8_tree_workspace bytes (uint8), by default taken from the
+        allocator for this call, like oasis_q8_attn's."""
+        R, table, lens = self._table(page_table, seq_len)
+        dt = q.dtype
+        if dt is not torch.bfloat16 and dt is not torch.float16:
+            raise ValueError(f"q must be bfloat16 or float16, got {dt}")
+        N = q.shape[1] if q.dim() == 4 else -1
+        shape = (R, N, self._Hq, 128)
+        qp = _want("q", q, dt, shape, self._dev)
+        o = _want("out", out, torch.float32 if self._out_fp32 else dt, shape, self._dev)
+        w = _want("tree", tree, torch.int64, (R, N), self._dev)
+        sz = None if tree_size is None else _want("tree_size", tree_size, torch.int32, (R,), self._dev)
+        st = _stream_on(stream, self._dev)
+        if workspace is None:
+            n = self._scratch.get((R, N, "tree"))
+            if n is None:
+                n = self._scratch[R, N, "tree"] = self.oasis_q8_tree_workspace(R, N) if 1 <= N <= 64 else 0
+            if n:
+                workspace = self._scratch_on(n, stream)
+        else:
+            n = workspace.numel()
+        ws = _want("workspace", workspace, torch.uint8, (n,), self._dev) if n else None
+        self._check(self._lib.oasis_q8_tree_attn(self.q8, R, N, qp, _TYPES[dt], w, sz, table, lens, o, ws, n, st))
+
+    def oasis_q8_keep(self, page_table, seq_len, nodes, keep, num_nodes, tree_size=None, stream=None) -> None:
+        """nodes [R][M] and keep [R] int32: the nodes of each request's tree that stay, in order;
+        seq_len counts the whole trees still."""
+        R, table, lens = self._table(page_table, seq_len)
+        M = nodes.shape[1] if nodes.dim() == 2 else -1
+        sz = None if tree_size is None else _want("tree_size", tree_size, torch.int32, (R,), self._dev)
+        self._check(self._lib.oasis_q8_keep(
+            self.q8, R, num_nodes, sz, table, lens, _want("nodes", nodes, torch.int32, (R, M), self._dev),
+            _want("keep", keep, torch.int32, (R,), self._dev), M, _stream_on(stream, self._dev)))
+
+
+def oasis_token_logprobs(logits, tokens=None, logprobs=None, entropy=None, top_ids=None,
+                         top_logprobs=None, stream=None) -> None:
+    """logits [rows][V] (or [..., V] with evenly spaced rows) in bf16, fp16 or fp32, tokens [rows]
+    int32 (negative: the row is not wanted, its outputs stay); logprobs, entropy [rows] fp32,
+    top_ids [rows][k] int32 and top_logprobs [rows][k] fp32 are written where given."""
+    typ = _TYPES.get(logits.dtype)
+    if logits.dim() < 2 or typ is None or not logits.is_cuda:
+        raise ValueError("logits must be a bfloat16, float16 or float32 CUDA tensor [rows][V]")
+    V, dev = logits.shape[-1], logits.get_device()
+    st, lead = logits.stride(), logits.shape[:-1]
+    rows = lead.numel()
+    stride, ok, want = V, V <= 1 or st[-1] == 1, None
+    for d in range(len(lead) - 1, -1, -1):  # one distance between all rows
+        if lead[d] == 1:
+            continue
+        if want is None:
+            stride = st[d]
+        elif st[d] != want:
+            ok = False
+        want = st[d] * lead[d]
+    if rows and not ok:
+        raise ValueError("logits: rows must be contiguous and evenly spaced")
+
+    def get(name, t, dtype, shape):
+        return 0 if t is None else _want(name, t, dtype, shape, dev)
+
+    if logprobs is not None and tokens is None:
+        raise ValueError("logprobs needs tokens")
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs come together")
+    k = 0 if top_ids is None else top_ids.shape[-1]
+    a = _LOGPROBS_ARGS.pack(rows, V, typ, k, dev, logits.data_ptr(), stride,
+                            get("tokens", tokens, torch.int32, lead),
+                            get("logprobs", logprobs, torch.float32, lead),
+                            get("entropy", entropy, torch.float32, lead),
+                            get("top_ids", top_ids, torch.int32, (*lead, k)),
+                            get("top_logprobs", top_logprobs, torch.float32, (*lead, k)))
+    rc = lib().oasis_token_logprobs(a, _stream_on(stream, dev))
+    if rc != OASIS_OK:
+        m = lib().oasis_logprobs_error(a)
+        raise OasisError(rc, m.decode() if m else "oasis_token_logprobs: CUDA error")
 
 
 def oasis_verify_drafts(target, draft, tokens, u_accept, u_sample, out_tokens, n_accept,
