@@ -821,8 +821,8 @@ OASIS_API const char* oasis_rope_error(const oasis_rope* rope);
  * in another way.  q and q_out may be NULL (keys alone).  positions: dev
  * [num_axes][T] int64, any values.  Tokens with a negative slot are not
  * written; their queries are turned all the same.
- * Precision: an angle's error does not grow with its position (2^-23 of a
- * turn); turning is fp32, rounded once, to q_out's type and to codes: keys are
+ * Precision: an angle is off by at most 2^-27 of a
+ * turn for positions up to 2^32; turning is fp32, rounded once, to q_out's type and to codes: keys are
  * not rounded to `type` between.  A row whose largest value comes within
  * fp32's rounding of a border of two exponents may get either.  The values are
  * oasis_q8_write's. */
@@ -850,7 +850,8 @@ OASIS_API int oasis_q8_tree_attn(oasis_q8* q8, int num_requests, int num_nodes, 
 /* Scratch that oasis_q8_tree_attn wants for these sizes (device memory,
  * 256-byte aligned; 0 is possible).  A call's scratch must not be given to
  * another that may run at the same time. */
-OASIS_API int oasis_q8_tree_workspace(const oasis_q8* q8, int num_requests, int num_nodes, size_t* bytes);
+OASIS_API int oasis_q8_tree_workspace(const oasis_q8* q8, int num_requests, int num_nodes, int type,
+                                      size_t* bytes);
 
 /* Keep some nodes of each request's tree: for i < keep[r] the keys and values
  * of node nodes[r][i] move to node i's place (codes and exponents as they are;

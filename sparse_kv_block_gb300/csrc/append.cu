@@ -26,8 +26,8 @@ __device__ __forceinline__ void put(__half* p, const float (&x)[4]) {
 //
 // The angle.  A position times a frequency, in turns, is taken modulo one as
 // 64-bit integers: a frequency is a multiple of 2^-64 turns, so the product is
-// exact whatever the position, and its upper 32 bits are the angle.  (In fp32
-// a position of 10^6 would be off by 2^-4 radians.)  cos and sin of a pair are
+// exact whatever the position.  (In fp32 a position of 10^6 would be off by 2^-4
+// radians.)  cos and sin of a pair are
 // made once for all of the token's heads that the warp has.
 template <typename T>
 __device__ __forceinline__ void turn_item(const AppendArgs& a, int64_t pair, int chunk, int lane) {
@@ -47,9 +47,19 @@ __device__ __forceinline__ void turn_item(const AppendArgs& a, int64_t pair, int
     if (there && turns) {
       const uint64_t phase =
           static_cast<uint64_t>(a.positions[a.axis[4 * c + i] * static_cast<int64_t>(kv.T) + t]) * a.turn[4 * c + i];
-      // Half turns in [-1, 1).
-      const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-      sincospif(x, &sn[i], &cs[i]);
+      // The nearest quarter turn, and what is left of the angle, an eighth of a
+      // turn at most, in half turns: so fp32 holds it to 2^-28 of a turn.
+      const uint32_t quarter_turn = (static_cast<uint32_t>(phase >> 32) + 0x20000000u) >> 30;
+      const int32_t rest = static_cast<int32_t>(
+          static_cast<int64_t>(phase - (static_cast<uint64_t>(quarter_turn) << 62)) >> 30);
+      float s, c;
+      sincospif(static_cast<float>(rest) * 0x1p-33f, &s, &c);
+      cs[i] = quarter_turn & 1 ? -s : c;
+      sn[i] = quarter_turn & 1 ? c : s;
+      if (quarter_turn & 2) {
+        cs[i] = -cs[i];
+        sn[i] = -sn[i];
+      }
       cs[i] *= a.scale;
       sn[i] *= a.scale;
     }

@@ -65,6 +65,18 @@ struct TreeArgs {
   int type, out_fp32;
   float scale_log2;
   long long wait_limit;
+  // Shares of pairs that several CTAs have: average (in units of 2^8), (m, sum).
+  float* part;               // [2 ctas][part_rows][d]: of the pair that a CTA finds begun, and of its last one
+  float2* stat;
+  int4* info;                // [ctas]: the pair that begins there and goes on (r, h, block, shares), r -1: none
+  int ctas, part_rows;
+};
+
+// Launch and scratch of the tree attention.
+struct TreeShape {
+  int tiles;                 // of 128 rows a CTA, 1 or 2
+  int ctas, rows;
+  size_t part_bytes, stat_bytes, bytes;
 };
 
 struct LogprobsArgs {
@@ -187,7 +199,9 @@ cudaError_t launch_join(const PrefixArgs& a, cudaStream_t s);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 cudaError_t launch_q8_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_q8_keep(const KeepArgs& a, cudaStream_t s);
-cudaError_t launch_q8_tree(const TreeArgs& a, cudaStream_t s);
+TreeShape tree_shape(int R, int N, int G, int Hkv, int max_blocks, int type);
+// The map covers the pages' keys, [pages][Hkv][2 (even, odd tokens)][8][128 bytes], with boxes of one unit's.
+cudaError_t launch_q8_tree(const TreeArgs& a, int tiles, const CUtensorMap& map, cudaStream_t s);
 cudaError_t launch_logprobs(const LogprobsArgs& a, cudaStream_t s);
 
 // Load the kernels' code (and set their shared memory) on the current device.

@@ -61,6 +61,34 @@ class OnDevice {
   cudaError_t e_;
 };
 
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static const auto encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  return encode;
+}
+
+// A map of the pages' keys [pages][Hkv][2 (even, odd tokens)][8][128 bytes]
+// with boxes of a unit's: its even tokens' rows, then its odd ones'.
+bool key_map(const oasis_q8_config& cfg, void* pages, CUtensorMap* map) {
+  const auto encode = map_encoder();
+  if (!encode) return false;
+  const cuuint64_t head = kQ8UnitBytes, page = head * cfg.num_kv_heads;
+  const cuuint64_t dims[5] = {kHeadDim, kBlock / 2, 2, static_cast<cuuint64_t>(cfg.num_kv_heads),
+                              static_cast<cuuint64_t>(cfg.num_pages)};
+  const cuuint64_t strides[4] = {2 * kHeadDim, kHeadDim, head, page};
+  const cuuint32_t box[5] = {kHeadDim, kBlock / 2, 2, 1, 1}, one[5] = {1, 1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, pages, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 struct oasis_q8 {
@@ -70,6 +98,7 @@ struct oasis_q8 {
   uint8_t* pages = nullptr;
   uint32_t* err = nullptr;
   long long wait_limit = kWaitLimitCycles;
+  CUtensorMap keys{};  // of the tree attention
   char last_error[256] = "";
 
   int fail(int code, const char* fmt, ...) {
@@ -110,8 +139,11 @@ OASIS_API int oasis_q8_init(const oasis_q8_config* cfg, void* pages, void* works
   if (cudaDeviceSynchronize() != cudaSuccess) return OASIS_ECUDA;
   // (A memset may return early; the caller's streams need not wait for it.)
   if (cudaMemset(workspace, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return OASIS_ECUDA;
+  CUtensorMap keys;
+  if (!key_map(*cfg, pages, &keys)) return OASIS_ECUDA;
   oasis_q8* q = new (std::nothrow) oasis_q8;
   if (!q) return OASIS_ENOMEM;
+  q->keys = keys;
   q->cfg = *cfg;
   q->G = cfg->num_q_heads / cfg->num_kv_heads;
   const float scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.f / std::sqrt(static_cast<float>(kHeadDim));
@@ -257,15 +289,7 @@ int attn_args(oasis_q8* q8, const char* who, int R, int S, int causal, const voi
 // A map of a prefix [Hkv][blocks][2][B][d] with boxes of 8 blocks' keys or
 // values, 64 dims: 128 tokens of 128 bytes.  Blocks past the end read as 0.
 int prefix_map(oasis_q8* q8, const void* kv, int blocks, CUtensorMap* map) {
-  static const auto encode = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-  }();
+  const auto encode = map_encoder();
   if (!encode) return q8->fail(OASIS_ECUDA, "cuTensorMapEncodeTiled unavailable");
   const cuuint64_t dims[5] = {kHeadDim, kBlock, 2, static_cast<cuuint64_t>(blocks),
                               static_cast<cuuint64_t>(q8->cfg.num_kv_heads)};
@@ -449,14 +473,15 @@ OASIS_API const char* oasis_rope_error(const oasis_rope* r) {
 
 namespace {
 
-// A frequency in radians as turns modulo one, in units of 2^-64: the product
-// with 1 / (2 pi), given in two doubles, to about 2^-100 of itself.
+// A frequency in radians as turns modulo one, in units of 2^-64 (cut to whole
+// ones): the product with 1 / (2 pi), given in two doubles.
 uint64_t turns(double radians) {
   constexpr double kInv = 0x1.45f306dc9c883p-3, kInvLow = -0x1.6b01ec5417056p-57;
   const double r = std::fabs(radians), hi = r * kInv;
   const double lo = std::fma(r, kInv, -hi) + r * kInvLow;
-  const uint64_t u = static_cast<uint64_t>(std::ldexp(hi - std::floor(hi), 64)) +
-                     static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(std::ldexp(lo, 64))));
+  const double whole = static_cast<double>(static_cast<int64_t>(hi));
+  const uint64_t u = static_cast<uint64_t>((hi - whole) * 0x1p64) +
+                     static_cast<uint64_t>(static_cast<int64_t>(lo * 0x1p64));
   return radians < 0 ? 0 - u : u;
 }
 
@@ -512,10 +537,13 @@ OASIS_API int oasis_q8_append(oasis_q8* q8, const oasis_rope* rope, const void* 
   return q8->cuda(launch_q8_append(a, static_cast<cudaStream_t>(stream)), "q8_append launch");
 }
 
-OASIS_API int oasis_q8_tree_workspace(const oasis_q8* q8, int num_requests, int num_nodes, size_t* bytes) {
-  if (!q8 || !bytes || num_requests < 0 || num_requests > 65535 || num_nodes < 1 || num_nodes > kTreeMaxNodes)
+OASIS_API int oasis_q8_tree_workspace(const oasis_q8* q8, int num_requests, int num_nodes, int type, size_t* bytes) {
+  if (!q8 || !bytes || num_requests < 0 || num_requests > 65535 || num_nodes < 1 || num_nodes > kTreeMaxNodes ||
+      (type != OASIS_BF16 && type != OASIS_FP16))
     return OASIS_EINVAL;
-  *bytes = 0;
+  *bytes = num_requests > 0
+               ? tree_shape(num_requests, num_nodes, q8->G, q8->cfg.num_kv_heads, q8->cfg.max_blocks, type).bytes
+               : 0;
   return OASIS_OK;
 }
 
@@ -537,10 +565,9 @@ OASIS_API int oasis_q8_tree_attn(oasis_q8* q8, int num_requests, int num_nodes, 
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(tree, 8) || !aligned(tree_size, 4) ||
       !aligned(page_table, 4) || !aligned(seq_len, 4))
     return q8->fail(OASIS_EINVAL, "q8_tree_attn: misaligned pointer (q, out: 16 bytes, tree: 8)");
-  size_t need = 0;
-  oasis_q8_tree_workspace(q8, num_requests, num_nodes, &need);
-  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
-    return q8->fail(OASIS_EINVAL, "q8_tree_attn: workspace null, misaligned (256 bytes) or under %zu bytes", need);
+  const TreeShape sh = tree_shape(num_requests, num_nodes, q8->G, q8->cfg.num_kv_heads, q8->cfg.max_blocks, type);
+  if (!workspace || workspace_bytes < sh.bytes || !aligned(workspace, 256))
+    return q8->fail(OASIS_EINVAL, "q8_tree_attn: workspace null, misaligned (256 bytes) or under %zu bytes", sh.bytes);
   OnDevice dev(q8->cfg.device);
   if (int rc = q8->cuda(dev.error(), "cudaSetDevice")) return rc;
   TreeArgs a{};
@@ -563,7 +590,13 @@ OASIS_API int oasis_q8_tree_attn(oasis_q8* q8, int num_requests, int num_nodes, 
   a.out_fp32 = q8->cfg.out_fp32;
   a.scale_log2 = q8->scale_log2;
   a.wait_limit = q8->wait_limit;
-  return q8->cuda(launch_q8_tree(a, static_cast<cudaStream_t>(stream)), "q8_tree_attn launch");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.part = reinterpret_cast<float*>(ws);
+  a.stat = reinterpret_cast<float2*>(ws + sh.part_bytes);
+  a.info = reinterpret_cast<int4*>(ws + sh.part_bytes + sh.stat_bytes);
+  a.ctas = sh.ctas;
+  a.part_rows = sh.rows;
+  return q8->cuda(launch_q8_tree(a, sh.tiles, q8->keys, static_cast<cudaStream_t>(stream)), "q8_tree_attn launch");
 }
 
 OASIS_API int oasis_q8_keep(oasis_q8* q8, int num_requests, int num_nodes, const int32_t* tree_size,

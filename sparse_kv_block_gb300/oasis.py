@@ -176,7 +176,7 @@ EXPORTS = {
     "oasis_q8_append": (c_int, [_P, POINTER(oasis_rope), _P, _P, _P, _P, c_int, c_int64, c_int64,
                                 c_int64, c_int64, _P, _P, c_int, _P]),
     "oasis_q8_tree_attn": (c_int, [_P, c_int, c_int, _P, c_int, _P, _P, _P, _P, _P, _P, c_size_t, _P]),
-    "oasis_q8_tree_workspace": (c_int, [_P, c_int, c_int, POINTER(c_size_t)]),
+    "oasis_q8_tree_workspace": (c_int, [_P, c_int, c_int, c_int, POINTER(c_size_t)]),
     "oasis_q8_keep": (c_int, [_P, c_int, c_int, _P, _P, _P, _P, _P, c_int, _P]),
     "oasis_logprobs_error": (c_char_p, [_P]),
     "oasis_token_logprobs": (c_int, [_P, _P]),
@@ -845,9 +845,9 @@ class Q8Cache:
             _want("positions", positions, torch.int64, shape, self._dev),
             _want("slots", slots, torch.int64, (T,), self._dev), T, _stream_on(stream, self._dev)))
 
-    def oasis_q8_tree_workspace(self, R: int, N: int) -> int:
+    def oasis_q8_tree_workspace(self, R: int, N: int, dtype=torch.bfloat16) -> int:
         n = c_size_t(0)
-        rc = lib().oasis_q8_tree_workspace(self.q8, R, N, ctypes.byref(n))
+        rc = lib().oasis_q8_tree_workspace(self.q8, R, N, _TYPES.get(dtype, -1), ctypes.byref(n))
         if rc != OASIS_OK:
             raise OasisError(rc, "q8_tree_workspace: bad size")
         return n.value
@@ -869,9 +869,9 @@ class Q8Cache:
         sz = None if tree_size is None else _want("tree_size", tree_size, torch.int32, (R,), self._dev)
         st = _stream_on(stream, self._dev)
         if workspace is None:
-            n = self._scratch.get((R, N, "tree"))
+            n = self._scratch.get((R, N, dt))
             if n is None:
-                n = self._scratch[R, N, "tree"] = self.oasis_q8_tree_workspace(R, N) if 1 <= N <= 64 else 0
+                n = self._scratch[R, N, dt] = self.oasis_q8_tree_workspace(R, N, dt) if 1 <= N <= 64 else 0
             if n:
                 workspace = self._scratch_on(n, stream)
         else:

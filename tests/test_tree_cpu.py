@@ -50,7 +50,7 @@ def test_null_handles():
     r = rope()
     assert L.oasis_q8_append(None, ctypes.byref(r), 16, 16, 16, 16, 0, 256, 256, 256, 256, 16, 16, 1, None) == ob.OASIS_EINVAL
     assert L.oasis_q8_tree_attn(None, 1, 1, 16, 0, 16, None, 16, 16, 16, None, 0, None) == ob.OASIS_EINVAL
-    assert L.oasis_q8_tree_workspace(None, 1, 1, None) == ob.OASIS_EINVAL
+    assert L.oasis_q8_tree_workspace(None, 1, 1, 0, None) == ob.OASIS_EINVAL
     assert L.oasis_q8_keep(None, 1, 1, None, 16, 16, 16, 16, 1, None) == ob.OASIS_EINVAL
     assert L.oasis_token_logprobs(None, None) == ob.OASIS_EINVAL
 
