@@ -70,6 +70,7 @@ struct TreeArgs {
   float2* stat;
   int4* info;                // [ctas]: the pair that begins there and goes on (r, h, block, shares), r -1: none
   int ctas, part_rows;
+  uint32_t over_G;           // 2^16 / G + 1: row / G is row * over_G >> 16 (exact for the rows of 64 nodes, G to 8)
 };
 
 // Launch and scratch of the tree attention.

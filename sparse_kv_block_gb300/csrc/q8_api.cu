@@ -596,6 +596,7 @@ OASIS_API int oasis_q8_tree_attn(oasis_q8* q8, int num_requests, int num_nodes, 
   a.info = reinterpret_cast<int4*>(ws + sh.part_bytes + sh.stat_bytes);
   a.ctas = sh.ctas;
   a.part_rows = sh.rows;
+  a.over_G = 65536u / q8->G + 1;
   return q8->cuda(launch_q8_tree(a, sh.tiles, q8->keys, static_cast<cudaStream_t>(stream)), "q8_tree_attn launch");
 }
 

@@ -30,6 +30,7 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t at, uint32_t leadin
 // Instruction descriptors: fp32 sums; 16-bit operands are fp16, or bf16 as
 // said; 8-bit ones e4m3; B as columns of N, or of K (transposed).
 constexpr uint32_t kMmaF32 = 1u << 4, kMmaBf16A = 1u << 7, kMmaBf16B = 1u << 10, kMmaTransposeB = 1u << 16;
+constexpr uint32_t kMmaScaleE8 = 1u << 23;  // (with scales only; no bit for fp32 sums then)
 constexpr uint32_t mma_shape(uint32_t M, uint32_t N) { return (N >> 3) << 17 | (M >> 4) << 24; }
 
 // Called by a whole warp, issued by its elected lane: descriptors that are
@@ -57,13 +58,24 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(kInstr), "r"(add), "r"(lead)
       : "memory");
 }
-// Eight-bit operands from shared memory, 32 columns a step.
+// Eight-bit operands from shared memory, 32 columns a step, with a power of two (a
+// biased exponent byte) for each row of A and of B, from tensor memory.
 template <uint32_t kInstr>
-__device__ __forceinline__ void mma_ss_8bit(uint32_t d, uint64_t a, uint64_t b, uint32_t add, uint32_t lead) {
+__device__ __forceinline__ void mma_ss_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t scale_a, uint32_t scale_b,
+                                              uint32_t add, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 e, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kInstr), "r"(add), "r"(lead)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 e, %7, 0;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kInstr), "r"(scale_a), "r"(scale_b), "r"(add), "r"(lead)
+      : "memory");
+}
+// 128 rows' exponents, a word a row (its byte four times), from shared memory
+// [32][4] (row 32 c + i at [i][c]) to four columns of tensor memory.
+__device__ __forceinline__ void load_scales(uint32_t at, uint64_t desc, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %2, 0;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(at),
+      "l"(desc), "r"(lead)
       : "memory");
 }
 // Arrive on `bar` when the elected lane's products so far are done.
@@ -102,6 +114,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
       "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
       "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
