@@ -9,10 +9,17 @@
 //
 // The k largest.  Entries are ordered by (value, then lower index), as 64-bit
 // keys, so no two are equal.  The k-th largest of the threads' own largest
-// entries is no more than the row's k-th largest entry, and only the k threads
-// whose largest reach it can hold entries that do: their entries alone (a few
-// hundred) are read again, from the L2, and those that reach it are ranked by
-// counting.  Nothing depends on the order in which threads get there.
+// entries is no more than the row's k-th largest entry.  Every thread keeps the
+// largest of each of 16 slots of its entries too: the slots that reach that
+// threshold (some k of them) are read again, and their entries that reach it are
+// ranked by counting.  Nothing depends on the order in which threads get there.
+//
+// Bound by memory, and by its integer and fp32 pipes in 16-bit types (some four
+// operations an entry); a thread's next four pieces are on their way while four
+// are looked at.  GB300, 512 rows of 151936, bf16: k = 0 41 us, 1 42, 20 44 (3.5
+// TB/s); fp32, k = 20, 75 (4.1 TB/s).  Before: without the next pieces on their
+// way and packed arithmetic 47; the entries of the k threads read again, 20 us
+// more at k = 20 (16 bytes of each sector of memory that has left the L2).
 #include <cuda_fp16.h>
 
 #include "q8.cuh"
@@ -21,8 +28,14 @@
 namespace oasis {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+// Warps a CTA: eight where the clusters of eight CTAs of all rows run at once (a
+// row's latency counts), else four, whose CTAs fill the SMs more evenly.  GB300,
+// us with four and eight: 4 rows of 32000, k = 5, 11.1, 9.9; 1 of 151936, k = 1,
+// 17.0, 15.0; 64 of 128256, k = 20, 27.3, 33.4 (two rounds).
+constexpr int kFewRows = 8, kManyRows = 4;
+template <int kWarps>
+constexpr int kPerSM = 28 / kWarps;  // CTAs
+constexpr int kBatch = 4, kSlots = 16;
 constexpr int kTop = kLogprobsMaxTop;
 constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
@@ -129,37 +142,100 @@ struct Seen {
   int piece = -1;
 };
 
-template <int kN, int kPieces>
-__device__ __forceinline__ void take(Seen& t, const float (&x)[kPieces][kN], int j0, int step) {
+// Two entries a word, their largest, and as floats (an fp32 row: one a word).
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, const __nv_bfloat16*) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, const __half*) {
+  const __half2 m = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+template <typename T>
+__device__ __forceinline__ float largest_of(const uint4& w) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmax3(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z)), __uint_as_float(w.w));
+  } else {
+    const T* p = nullptr;
+    const uint32_t m = max2(max2(w.x, w.y, p), max2(w.z, w.w, p), p);
+    const T* v = reinterpret_cast<const T*>(&m);
+    return fmaxf(to_f(v[0]), to_f(v[1]));
+  }
+}
+
+template <typename T, int kPieces>
+__device__ __forceinline__ float take(Seen& t, const uint4 (&w)[kPieces], int j0, int step) {
   float top = -INFINITY;
 #pragma unroll
   for (int b = 0; b < kPieces; ++b) {
-    float m = x[b][0];
-#pragma unroll
-    for (int i = 1; i < kN; ++i) m = fmaxf(m, x[b][i]);
+    const float m = largest_of<T>(w[b]);
     if (m > t.best) {
       t.best = m;
       t.piece = j0 + b * step;
     }
     top = fmaxf(top, m);
   }
-  top *= kL;
-  if (top > t.a.m) {
-    lower(t.a, top);
-    t.a.m = top;
+  if (top * kL > t.a.m) {
+    lower(t.a, top * kL);
+    t.a.m = top * kL;
   }
   const float off = t.a.m == -INFINITY ? 0.f : -t.a.m;
-  float s[2] = {0.f, 0.f}, e[2] = {0.f, 0.f};
+  const uint64_t by = f2pack(kL, kL), off2 = f2pack(off, off);
+  uint64_t s[2] = {0, 0}, e[2] = {0, 0};
+  const T* p = nullptr;
 #pragma unroll
-  for (int b = 0; b < kPieces; ++b)
+  for (int b = 0; b < kPieces; ++b) {
+    float x[kPer<T>];
+    floats_of(w[b], p, x);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const float y = fmaf(x[b][i], kL, off), w = ex2(y);
-      s[i & 1] += w;
-      e[i & 1] = fmaf(w, fmaxf(y, -200.f), e[i & 1]);  // (0 times -inf would be NaN)
+    for (int i = 0; i < kPer<T>; i += 2) {
+      const uint64_t y2 = ffma2(f2pack(x[i], x[i + 1]), by, off2);
+      float y0, y1;
+      f2unpack(y2, y0, y1);
+      const uint64_t w2 = f2pack(ex2(y0), ex2(y1));
+      s[i >> 1 & 1] = fadd2(s[i >> 1 & 1], w2);
+      e[i >> 1 & 1] = ffma2(w2, y2, e[i >> 1 & 1]);
     }
-  t.a.s += s[0] + s[1];
-  t.a.e += e[0] + e[1];
+  }
+  t.a.s += f2sum(fadd2(s[0], s[1]));
+  float weighted = f2sum(fadd2(e[0], e[1]));
+  if (weighted != weighted) {  // an entry of -inf, 0 times it: again, with what has no weight held (or NaN, which stays)
+    weighted = 0.f;
+#pragma unroll
+    for (int b = 0; b < kPieces; ++b) {
+      float x[kPer<T>];
+      floats_of(w[b], p, x);
+#pragma unroll
+      for (int i = 0; i < kPer<T>; ++i) {
+        const float y = fmaf(x[i], kL, off);
+        weighted = fmaf(ex2(y), fmaxf(y, -200.f), weighted);
+      }
+    }
+  }
+  t.a.e += weighted;
+  return top;
+}
+// The same of one piece that may be partly outside the row.
+template <typename T>
+__device__ __forceinline__ float take_edge(Seen& t, const Row<T>& row, int j) {
+  float x[kPer<T>], most = -INFINITY;
+  row.entries(j, x);
+  for (int i = 0; i < kPer<T>; ++i) {
+    if (x[i] > t.best) {
+      t.best = x[i];
+      t.piece = j;
+    }
+    const float top = x[i] * kL;
+    if (top > t.a.m) {
+      lower(t.a, top);
+      t.a.m = top;
+    }
+    const float y = fmaf(x[i], kL, t.a.m == -INFINITY ? 0.f : -t.a.m), w = ex2(y);
+    t.a.s += w;
+    t.a.e = fmaf(w, fmaxf(y, -200.f), t.a.e);
+    most = fmaxf(most, x[i]);
+  }
+  return most;
 }
 
 // One step of a sorting network over the warp: the larger of each two at the
@@ -181,21 +257,24 @@ __device__ __forceinline__ uint64_t merge_down(uint64_t v, int lane) {
   return v;
 }
 
+template <int kWarps>
 struct Shared {
+  static constexpr int kThreads = kWarps * 32;
   Sums warp_sum[kWarps];
   uint64_t lists[kWarps][32];
   uint64_t candidates[kCandidates];
   uint64_t result[kTop];
-  uint64_t best;
-  int flagged[kTop];
-  int n_flagged, n_candidates;
+  float most[kSlots][kThreads];
+  uint16_t reached[kSlots * kThreads];
+  int n_reached, n_candidates;
   Sums sum;
 };
 
 // The k largest of sh.candidates into sh.result (sorted; 0 where there are
 // fewer).  Called by the whole CTA, result cleared.
-__device__ __forceinline__ void rank(Shared& sh, int n, int k) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+template <int kWarps>
+__device__ __forceinline__ void rank(Shared<kWarps>& sh, int n, int k) {
+  for (int i = threadIdx.x; i < n; i += kWarps * 32) {
     const uint64_t key = sh.candidates[i];
     int r = 0;
     for (int j = 0; j < n; ++j) r += sh.candidates[j] > key;
@@ -203,8 +282,9 @@ __device__ __forceinline__ void rank(Shared& sh, int n, int k) {
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void largest(Shared& sh, const Row<T>& row, const Seen& t, int k, int first, int total) {
+template <typename T, int kWarps>
+__device__ __forceinline__ void largest(Shared<kWarps>& sh, const Row<T>& row, const Seen& t, int k, int first, int total, int slot) {
+  constexpr int kThreads = kWarps * 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t own = 0;
   const int mine = first + threadIdx.x;
@@ -228,24 +308,36 @@ __device__ __forceinline__ void largest(Shared& sh, const Row<T>& row, const See
     __syncthreads();
   }
   const uint64_t least = sh.lists[0][k - 1];
-  if (own && own >= least) sh.flagged[atomicAdd(&sh.n_flagged, 1)] = mine;
+  if (k == 1) {
+    if (threadIdx.x == 0) sh.result[0] = least;
+    __syncthreads();
+    return;
+  }
+  // The slots that reach the threshold, and of their pieces the entries that do.
+  const uint32_t least_x = static_cast<uint32_t>(least >> 32);
+#pragma unroll 4
+  for (int i = 0; i < kSlots; ++i)
+    if (float_key(sh.most[i][threadIdx.x]) >= least_x)
+      sh.reached[atomicAdd(&sh.n_reached, 1)] = static_cast<uint16_t>(i * kThreads + threadIdx.x);
   __syncthreads();
-  const int n_flagged = sh.n_flagged;
-  auto each = [&](auto&& f) {  // the entries of the flagged threads, a warp a thread's
-    for (int i = warp; i < n_flagged; i += kWarps)
-      for (int j = sh.flagged[i] + lane * total; j < row.pieces; j += 32 * total) {
-        float x[kPer<T>];
-        const unsigned in = row.entries(j, x);
-#pragma unroll
-        for (int b = 0; b < kPer<T>; ++b)
-          if ((in >> b & 1) && x[b] == x[b]) f(key_of(x[b], j * kPer<T> - row.skew + b));
+  const int pieces = sh.n_reached * slot;
+  auto each = [&](auto&& f) {
+#pragma unroll 1
+    for (int e = threadIdx.x; e < pieces; e += kThreads) {
+      const int n = e / slot, at = sh.reached[n];
+      const int j = first + at % kThreads + (at / kThreads * slot + e - n * slot) * total;
+      if (j >= row.pieces || (row.whole(j) && float_key(largest_of<T>(row.raw(j))) < least_x)) continue;
+#pragma unroll 1
+      for (int i = max(j * kPer<T> - row.skew, 0); i < min((j + 1) * kPer<T> - row.skew, row.V); ++i) {
+        const float x = to_f(row.p[i]);
+        const uint64_t key = key_of(x, i);
+        if (x == x && key >= least) f(key);
       }
+    }
   };
   each([&](uint64_t key) {
-    if (key >= least) {
-      const int at = atomicAdd(&sh.n_candidates, 1);
-      if (at < kCandidates) sh.candidates[at] = key;
-    }
+    const int at = atomicAdd(&sh.n_candidates, 1);
+    if (at < kCandidates) sh.candidates[at] = key;
   });
   __syncthreads();
   if (sh.n_candidates <= kCandidates) {
@@ -272,9 +364,10 @@ __device__ __forceinline__ void largest(Shared& sh, const Row<T>& row, const See
   __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArgs a, int cluster) {
-  __shared__ Shared sh;
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kPerSM<kWarps>) logprobs_kernel(const LogprobsArgs a, int cluster) {
+  constexpr int kThreads = kWarps * 32;
+  __shared__ Shared<kWarps> sh;
   previous_done();
   next_may_begin();
   const int r = static_cast<int>(blockIdx.x / cluster);
@@ -284,31 +377,46 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   if (token < 0) return;  // every CTA of the cluster alike
   const Row<T> row(static_cast<const T*>(a.logits) + r * a.stride, a.V);
   if (tid < kTop) sh.result[tid] = 0;
-  if (tid == 0) sh.n_flagged = sh.n_candidates = 0;
+  if (tid == 0) sh.n_reached = sh.n_candidates = 0;
 
   const int total = cluster * kThreads, first = at * kThreads;
   Seen t;
+  // A thread's pieces in fours, in at most kSlots slots of so many each.
+  const int fours = (row.pieces + kBatch * total - 1) / (kBatch * total);
+  const int slot = (fours + kSlots - 1) / kSlots * kBatch;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) sh.most[i][tid] = -INFINITY;
+  auto whole = [&](int j) { return j >= row.begin && j + (kBatch - 1) * total < row.end; };
+  uint4 w[kBatch], next[kBatch];
+  auto load = [&](uint4 (&to)[kBatch], int j) {
+    if (whole(j))
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) to[b] = row.raw(j + b * total);
+  };
   int j = first + tid;
-  constexpr int kBatch = 4;
-  if (j < row.pieces && !row.whole(j)) {
-    float x[1][kPer<T>];
-    row.entries(j, x[0]);
-    take(t, x, j, 0);
-    j += total;
-  }
-  for (; j + (kBatch - 1) * total < row.end; j += kBatch * total) {
-    uint4 w[kBatch];
+  load(w, j);
+#pragma unroll 1
+  for (int n = 0, i = 0; n < fours; ++n) {
+    load(next, j + kBatch * total);
+    float top = -INFINITY;
+    if (whole(j)) {
+      top = take<T>(t, w, j, total);
+    } else {
+#pragma unroll 1
+      for (int at = j; at < min(j + kBatch * total, row.pieces); at += total) {
+        if (row.whole(at)) {
+          const uint4 one[1] = {row.raw(at)};
+          top = fmaxf(top, take<T>(t, one, at, 0));
+        } else {
+          top = fmaxf(top, take_edge(t, row, at));
+        }
+      }
+    }
+    sh.most[i][tid] = fmaxf(sh.most[i][tid], top);
+    if ((n + 1) * kBatch >= (i + 1) * slot) ++i;
+    j += kBatch * total;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) w[b] = row.raw(j + b * total);
-    float x[kBatch][kPer<T>];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) floats_of(w[b], row.p, x[b]);
-    take(t, x, j, total);
-  }
-  for (; j < row.pieces; j += total) {
-    float x[1][kPer<T>];
-    row.entries(j, x[0]);
-    take(t, x, j, 0);
+    for (int b = 0; b < kBatch; ++b) w[b] = next[b];
   }
 
   Sums sum = t.a;
@@ -319,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   sum = sh.warp_sum[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) sum = join(sum, sh.warp_sum[w]);
-  if (a.k > 0) largest(sh, row, t, a.k, first, total);
+  if (a.k > 0) largest(sh, row, t, a.k, first, total, slot);
 
   if (cluster > 1) {
     if (tid == 0) sh.sum = sum;
@@ -358,15 +466,26 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
   }
 }
 
-template <typename T>
-cudaError_t launch_t(const LogprobsArgs& a, cudaStream_t s) {
+template <typename T, int kWarps>
+cudaError_t launch_w(const LogprobsArgs& a, cudaStream_t s) {
   const int pieces = a.V / kPer<T> + 2;
   int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(a.rows) * cluster * 2 <= 4 * 152 &&
-         cluster * kThreads * 2 <= pieces)
+  while (cluster < kMaxCluster && static_cast<int64_t>(a.rows) * cluster * 2 <= kPerSM<kWarps> * 152 &&
+         cluster * kWarps * 32 * 2 <= pieces)
     cluster *= 2;
-  return launch_early(logprobs_kernel<T>, static_cast<unsigned>(a.rows) * cluster, kThreads, 0, s, cluster, a,
-                      cluster);
+  return launch_early(logprobs_kernel<T, kWarps>, static_cast<unsigned>(a.rows) * cluster, kWarps * 32, 0, s, cluster,
+                      a, cluster);
+}
+template <typename T>
+cudaError_t launch_t(const LogprobsArgs& a, cudaStream_t s) {
+  const bool few = static_cast<int64_t>(a.rows) * kMaxCluster <= kPerSM<kFewRows> * 152;
+  return few ? launch_w<T, kFewRows>(a, s) : launch_w<T, kManyRows>(a, s);
+}
+template <typename T>
+cudaError_t preload_t() {
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, logprobs_kernel<T, kFewRows>);
+  return e == cudaSuccess ? cudaFuncGetAttributes(&at, logprobs_kernel<T, kManyRows>) : e;
 }
 
 }  // namespace
@@ -379,10 +498,9 @@ cudaError_t launch_logprobs(const LogprobsArgs& a, cudaStream_t s) {
 }
 
 cudaError_t preload_logprobs_kernels() {
-  cudaFuncAttributes at;
-  cudaError_t e = cudaFuncGetAttributes(&at, logprobs_kernel<__nv_bfloat16>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, logprobs_kernel<__half>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, logprobs_kernel<float>);
+  cudaError_t e = preload_t<__nv_bfloat16>();
+  if (e == cudaSuccess) e = preload_t<__half>();
+  if (e == cudaSuccess) e = preload_t<float>();
   return e;
 }
 
