@@ -842,7 +842,14 @@ OASIS_API int oasis_q8_append(oasis_q8* q8, const oasis_rope* rope, const void* 
  * uint64.  Rows of out from n_r on are left as they are.  A node that sees
  * nothing, and those of a request with no tokens, give zeros; so do those of a
  * request with fewer tokens than nodes, which raises BAD_BLOCK_ID.
- * num_requests <= 65535, R * N * Hq < 2^31. */
+ * num_requests <= 65535, R * N * Hq < 2^31.
+ * Precision: scores, maxima and sums are fp32; a query's entries count to 2^-19
+ * of its row's largest (exactly those within 2^-10 of it in bf16, 2^-7 in fp16).
+ * Weights are fp16 (2^-11 each; those under 2^-32 of the largest are lost),
+ * values are kept to 2^-39 of 448 times the largest power of two among them.
+ * A query row with a NaN or an infinity gives NaN; NaN keys and values count
+ * only for the nodes that see them.  The sum of |q_d k_d| has to stay under
+ * 2^127 and scores in fp32's range, as in oasis_q8_attn. */
 OASIS_API int oasis_q8_tree_attn(oasis_q8* q8, int num_requests, int num_nodes, const void* q, int type,
                                  const uint64_t* tree, const int32_t* tree_size,
                                  const int32_t* page_table, const int32_t* seq_len, void* out,

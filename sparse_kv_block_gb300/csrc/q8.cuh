@@ -36,11 +36,11 @@ __host__ __device__ __forceinline__ int q8_value_at(int j, int i) {
   return kQ8HalfBytes + i * kBlock + j;
 }
 
-// The least e with amax <= 448 * 2^e, held in [kQ8MinExp, kQ8MaxExp];
+// The least e with amax <= 448 * 2^e, held in [lowest, kQ8MaxExp];
 // `bits` are those of amax >= 0 (fp32).  448 = 1.75 * 2^8.
-__device__ __forceinline__ int q8_exponent(uint32_t bits) {
+__device__ __forceinline__ int q8_exponent(uint32_t bits, int lowest = kQ8MinExp) {
   const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return min(max(e, kQ8MinExp), kQ8MaxExp);
+  return min(max(e, lowest), kQ8MaxExp);
 }
 
 // 2^e for -126 <= e <= 127.

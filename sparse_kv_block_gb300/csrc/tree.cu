@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
           for (int off = 4; off; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
           const bool finite_row = amax < 0x7f800000u;
-          const int e = q8_exponent(finite_row ? amax : 0);
+          const int e = q8_exponent(finite_row ? amax : 0, -126);
           if ((lane & 7) == 0) {
             reinterpret_cast<uint32_t*>(smem + Lay::kQueryScale)[(row >> 7) * 128 + (row & 31) * 4 + (row >> 5 & 3)] =
                 (e + 127) * 0x01010101u;
