@@ -288,9 +288,8 @@ __device__ __forceinline__ void largest(Shared<kWarps>& sh, const Row<T>& row, c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t own = 0;
   const int mine = first + threadIdx.x;
-  if (mine < row.pieces) {
+  for (int j = t.piece >= 0 ? t.piece : mine; j < row.pieces && !own; j += total) {  // (nothing above -inf: the first of them)
     float x[kPer<T>];
-    const int j = t.piece >= 0 ? t.piece : mine;  // (nothing above -inf: the first of them)
     const unsigned in = row.entries(j, x);
 #pragma unroll
     for (int i = kPer<T> - 1; i >= 0; --i)
