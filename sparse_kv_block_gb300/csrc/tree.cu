@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const volatile Plan& plan = plans[k % kPlans];
       const int n = ok ? plan.n : 0, rows = plan.rows;
       const bool two = kTiles == 2 && rows > kTile;
-      // The segment's queries: half a warp a row, the next one's on its way.  (The
+      // The segment's queries: eight lanes a row, the next ones on their way.  (The
       // last ones' products are done: every stream has waited for its own.)
       if (n > 0) {
         const T* q_row = static_cast<const T*>(a.q) + plan.query + (lane & 7) * 16;
