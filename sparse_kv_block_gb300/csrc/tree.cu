@@ -34,17 +34,18 @@
 // end.  A job is 128 rows x 64 tokens; its scores are in one of three buffers of
 // tensor memory, where its weights take their place.
 //
-// GB300, us: 16 requests x 64 nodes x 32 / 8 heads over 16384 tokens 252 (tensor
+// GB300, us: 16 requests x 64 nodes x 32 / 8 heads over 16384 tokens 243 (tensor
 // cores 146 at the measured bf16 rate), 24 ragged ones up to 9001 tokens, fp16,
 // 73, one of 16 nodes over 4096 21.  What holds it back is a job's way through
 // the buffers (scores 400 cycles, the softmax of its 64 columns 700 to 1000,
-// outputs 270, 100 to 300 from each hand to the next): 1000 cycles a job where
+// outputs 270, 100 to 300 from each hand to the next): 960 cycles a job where
 // the products alone take 640.  Measured on the way, the first case: 128 columns a
 // job and two buffers 288; two buffers for scores and three for weights, released
 // as soon as they are read, 278; sixteen softmax warps 317; more registers for
 // the softmax warps (setmaxnreg) spilled.  The elected lane must not change in
 // the issuing loops: a lane that turned 0 when a wait had run out cost 460 cycles
-// a job, 282 in all.
+// a job, 282 in all; outputs' products unrolled over a tile's jobs 252 (their code
+// is fetched in turn with seven other roles').
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -452,13 +453,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (n == 0) break;
       // A tile's jobs: of the streams in turn, the even or the odd tokens, each in
       // the buffer that follows the last one's.
-      auto tile = [&](int i, auto streams) {
-        constexpr int kStreams = decltype(streams)::value;
+      const int jobs = two ? 4 : 2;
+      for (int i = 0; i < n; ++i, ++g) {
         const uint32_t st = g % Lay::kC;
         wait(half_full + st, (g / Lay::kC) & 1);
-#pragma unroll
-        for (int j = 0; j < 2 * kStreams; ++j) {
-          const uint32_t odd = j / kStreams;
+#pragma unroll 1
+        for (int j = 0; j < jobs; ++j) {
+          const uint32_t odd = two ? j >> 1 : j;
           const uint64_t v = v_desc + st * (kHalfStage >> 4) + odd * (2048 >> 4);
           const uint32_t to = kOutAt + (j & 1) * 128, from = buffer * 64;
           wait(p_full + buffer, parity);
@@ -471,11 +472,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           buffer = buffer == 2 ? 0 : buffer + 1;
         }
         mma_commit(half_empty + st, lead);
-      };
-      if (two)
-        for (int i = 0; i < n; ++i, ++g) tile(i, std::integral_constant<int, 2>{});
-      else
-        for (int i = 0; i < n; ++i, ++g) tile(i, std::integral_constant<int, 1>{});
+      }
     }
     // No product may outlive its operands and accumulators, either.
     mma_commit(drain, elected());
