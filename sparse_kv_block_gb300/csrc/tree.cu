@@ -683,7 +683,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         };
         auto load = [&](int row) {
           const int at = row0 + row, node = static_cast<int>(at * a.over_G >> 16);
-          const uint4* p = reinterpret_cast<const uint4*>(q_row + (node * a.Hq + at - node * a.G) * kHeadDim);
+          const uint4* p =
+              reinterpret_cast<const uint4*>(q_row + (node * a.Hq + at - node * a.G) * static_cast<int64_t>(kHeadDim));
           return row < rows ? Part{__ldg(p), __ldg(p + 1)} : Part{};
         };
         int row = warp * 4 + (lane >> 3);
