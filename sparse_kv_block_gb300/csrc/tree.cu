@@ -53,6 +53,7 @@
 #include "q8.cuh"
 #include "q8.h"
 #include "tcgen05.cuh"
+#include "tree_place.h"
 
 namespace oasis {
 namespace {
@@ -301,11 +302,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int from = __ffs(found) - 1;
         walk.q = {__shfl_sync(0xffffffffu, own.len, from), __shfl_sync(0xffffffffu, own.nodes, from),
                   __shfl_sync(0xffffffffu, own.blocks, from), __shfl_sync(0xffffffffu, own.tiles, from)};
-        // (Of one request: under 2^31.)
-        const int in = __shfl_sync(0xffffffffu, static_cast<int>(u0 - (incl - t)), from);
+        const TreePlace at = tree_place(__shfl_sync(0xffffffffu, u0 - (incl - t), from), walk.q.tiles);
         walk.r = r0 + from;
-        walk.pair = in / walk.q.tiles;
-        walk.i0 = in - walk.pair * walk.q.tiles;
+        walk.pair = at.pair;
+        walk.i0 = at.tile;
         break;
       }
       const int64_t before = __shfl_sync(0xffffffffu, incl, 31);
