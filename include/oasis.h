@@ -845,8 +845,11 @@ OASIS_API int oasis_q8_append(oasis_q8* q8, const oasis_rope* rope, const void* 
  * num_requests <= 65535, R * N * Hq < 2^31.
  * Precision: scores, maxima and sums are fp32; a query's entries count to 2^-19
  * of its row's largest (exactly those within 2^-10 of it in bf16, 2^-7 in fp16).
- * Weights are fp16 (2^-11 each; those under 2^-32 of the largest are lost),
- * values are kept to 2^-39 of 448 times the largest power of two among them.
+ * Weights are fp16 (2^-11 each, or 2^-32 of the row's largest where that is
+ * more).  Values of a context are kept to 2^-39 of 448 times the largest power
+ * of two among theirs.  What nodes hold that a row does not see costs it
+ * nothing: where powers of two near a tree are more than 20 apart, weighted
+ * values are kept to 2^-32 of 448 times the largest one that the row sees.
  * A query row with a NaN or an infinity gives NaN; NaN keys and values count
  * only for the nodes that see them.  The sum of |q_d k_d| has to stay under
  * 2^127 and scores in fp32's range, as in oasis_q8_attn. */

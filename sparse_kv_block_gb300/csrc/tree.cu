@@ -18,6 +18,8 @@
 //   without a swizzle for 16 rows of 8-bit weights.  Weights of 8 bits would be
 //   too coarse, so four warps turn the values into fp16, in units of the
 //   largest value exponent so far, and the weights are fp16 (tensor memory).
+//   In the tree's own tiles a row's unit is held to what the row sees, so that
+//   no other node's exponent costs it bits.
 //
 // One CTA an SM.  The tiles of all (request, KV head, 256 rows) are one
 // sequence, which the CTAs share out evenly, whatever the lengths: a CTA's range
@@ -71,6 +73,7 @@ constexpr int kSoftmaxThreads = kSoftmaxWarps * 32, kConvertThreads = 128;
 constexpr float kWeight = 7.f;                          // a weight is 2^(x - m + 7): 2^7 where the maximum is its own
 constexpr float kMostSum = 32768.f;                     // of a row's weights over a tile, each under it
 constexpr int kValueUp = 6;                             // a value is code * 2^(e - U + 6), at most 448 * 64
+constexpr int kReach = 14 + kValueUp;                   // U - e up to which that is a code times one fp16 number, exactly
 
 template <int kTerms, int kTiles>
 struct TreeLayout {
@@ -81,7 +84,7 @@ struct TreeLayout {
   static constexpr int kValues = kHalves + kC * kHalfStage;
   static constexpr int kKeyScale = kValues + kV * kValueStage;  // [kC][2][32][4] words: of even, of odd tokens' keys
   static constexpr int kQueryScale = kKeyScale + kC * 1024;     // [kTiles][32][4]
-  static constexpr int kInfo = kQueryScale + kTiles * 512;         // [kC] int4: first token, whole, U, -; valid tokens
+  static constexpr int kInfo = kQueryScale + kTiles * 512;         // [kC] int4: first token, whole, U, wide; valid tokens
   static constexpr int kNan = kInfo + kC * 32;                  // [kC + 1][128] words, then [kC + 1] int4 flags
   static constexpr int kNanFlag = kNan + (kC + 1) * kHeadDim * 8;
   static constexpr int kFactor = kNanFlag + (kC + 1) * 16;      // [kTiles][128] of a row's scores
@@ -90,7 +93,8 @@ struct TreeLayout {
   static constexpr int kHalfScale = kPlan + 4 * 64;             // [2][128] half: of a token's value
   static constexpr int kValid = kHalfScale + 2 * kTile * 2;     // [kV][8] tokens of a unit
   static constexpr int kConvert = kValid + kV * kUnits * 4;     // [4] int2 of the converting warps
-  static constexpr int kBars = kConvert + 32;
+  static constexpr int kExps = kConvert + 32;                   // [kC][128] bytes: values' exponents of even, of odd tokens
+  static constexpr int kBars = kExps + kC * kTile;
   static constexpr int kBytes = kBars + 384 + 1024;             // + alignment
   static_assert(kBytes <= 227 * 1024, "shared memory");
   static_assert(kHalves % 128 == 0 && kValues % 128 == 0 && kKeyScale % 128 == 0 && kBars % 8 == 0, "alignment");
@@ -580,7 +584,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           U = max(U, s.x >= 0 ? s.x : s.x + 1024);
           least = min(least, s.y);
         }
-        // 2^(e - U + 6), as two factors where fp16 does not hold it.
+        // 2^(e - U + 6), as two factors where fp16 does not hold it.  In a tile that
+        // rows see parts of, U may come from tokens that a row does not see.  If some
+        // are more than 2^kReach below it the tile is wide: all keep their bits, as
+        // codes times 2^(max(e - U, -kReach) + 6), and the rows' weights take the rest.
+        const bool seen_by_all = all_valid && t0 + kTile <= base, far = U - least > kReach;
         const int up = ve - U + kValueUp;
         const int place = unit * kBlock + (j & 1) * 8 + (j >> 1);  // even tokens, then odd ones
         half_scale[place] = valid ? pow2h(max(up, -14)) : 0;
@@ -588,14 +596,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int column = unit * 8 + (j >> 1);                    // of the scores of its kind
         reinterpret_cast<uint32_t*>(smem + Lay::kKeyScale)[st * 256 + (j & 1) * 128 + (column & 31) * 4 + (column >> 5)] =
             (valid ? ke : 127) * 0x01010101u;
+        if (far && !seen_by_all) (smem + Lay::kExps)[st * kTile + (j & 1) * 64 + column] = static_cast<uint8_t>(ve);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (d == 0)
-          reinterpret_cast<int4*>(smem + Lay::kInfo)[2 * st] = make_int4(t0, all_valid && t0 + kTile <= base, U, 0);
+          reinterpret_cast<int4*>(smem + Lay::kInfo)[2 * st] = make_int4(t0, seen_by_all, U, far && !seen_by_all);
         if (lane == 0) reinterpret_cast<uint32_t*>(smem + Lay::kInfo)[st * 8 + 4 + warp - kConvertWarp] = have_s;
         named_barrier<2, kConvertThreads>();
         if (lane == 0) mbar_arrive(scale_full + st);
         // Then a thread a dim.
-        const bool small = least - U + kValueUp < -14, tail = t0 + kTile > base;
+        const bool small = far && seen_by_all, tail = t0 + kTile > base;
         uint8_t* to = smem + Lay::kHalves + st * kHalfStage + d * 16;
         if (!all_valid || tail) {
           // A NaN code times a zero weight is NaN.  So codes past the end are
@@ -666,6 +675,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     };
     float* factor = reinterpret_cast<float*>(smem + Lay::kFactor);
     float4* stat = reinterpret_cast<float4*>(smem + Lay::kStat);
+    const uint8_t* exps = smem + Lay::kExps;
     int g = 0;                   // tiles so far
     for (int k = 0;; ++k) {
       ok = plan_there(k);
@@ -816,8 +826,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               float alpha = m == -INFINITY ? 0.f : ex2(m - to);
               m = to;
               l *= alpha;
-              alpha *= pow2_held(U - info.z);
-              U = info.z;
+              // A row's U: the tile's, but no more than kReach above what the row sees.
+              int to_U = info.z;
+              if (!all_seen) {
+                if ((see[0] | see[1]) == 0) {
+                  to_U = U;
+                } else if (info.w) {
+                  int most = 0;
+#pragma unroll 1
+                  for (uint64_t left = see[0] | static_cast<uint64_t>(see[1]) << 32; left; left &= left - 1)
+                    most = max(most, exps[st * kTile + odd * 64 + __ffsll(static_cast<long long>(left)) - 1]);
+                  to_U = max(U, min(to_U, most + kReach));
+                }
+              }
+              alpha *= pow2_held(U - to_U);
+              U = to_U;
               if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                 // (The last job's product may still run: only that of the one before
                 // was issued ahead of these scores.)
@@ -854,6 +877,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           l += sum;
           tmem_st32(at, w);
           tmem_wait_st();
+          if (info.w) {
+            // A wide tile: 2^(min(the tile's U, e + kReach) - the row's U), at most 1 where
+            // the row sees the token.
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 16) {
+              float o[16];
+              tmem_ld16(at + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const uint8_t* e = exps + st * kTile + odd * 64 + 2 * (c + j);
+                const uint32_t f2 = pow2h(min(min(info.z, e[0] + kReach) - U, 0)) |
+                                    static_cast<uint32_t>(pow2h(min(min(info.z, e[1] + kReach) - U, 0))) << 16;
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[j]), *reinterpret_cast<const __half2*>(&f2));
+                o[j] = *reinterpret_cast<const float*>(&y);
+              }
+              tmem_st16(at + c, reinterpret_cast<const uint32_t*>(o));
+            }
+            tmem_wait_st();
+          }
         }
         fence_before();
         __syncwarp();
