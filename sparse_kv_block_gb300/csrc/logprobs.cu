@@ -5,7 +5,9 @@
 //   log p_i = (x_i - m) - log S,   H = log S - sum e^(x - m) (x - m) / S,
 // both from one pass that keeps m, S and the weighted sum (in powers of two),
 // and every thread's largest entry.  H is a sum of two terms >= 0, so nothing
-// cancels.
+// cancels.  m is kept as it is, and x - m formed before anything else: a product
+// with log2 e would be off by more than whole powers of two from |x| of 10^8 on
+// and overflow near the type's largest, where masks are.
 //
 // The k largest.  Entries are ordered by (value, then lower index), as 64-bit
 // keys, so no two are equal.  The k-th largest of the threads' own largest
@@ -41,15 +43,15 @@ constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
 constexpr float kL = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// A sum of 2^(x L - m) and one of 2^(x L - m) (x L - m), m the largest x L.
+// A sum of 2^y and one of 2^y y, y = (x - m) L, m the largest x.
 struct Sums {
   float m, s, e;
 };
-// Its terms in units of 2^m2 >= 2^m.  (What has seen nothing above -inf has m =
+// Its terms in units of e^m2 >= e^m.  (What has seen nothing above -inf has m =
 // -inf and zeros, or NaN, which is kept.)
 __device__ __forceinline__ void lower(Sums& a, float m2) {
   if (a.m == -INFINITY || a.m == m2) return;
-  const float d = fmaxf(a.m - m2, -300.f), f = ex2(d);
+  const float d = fmaxf((a.m - m2) * kL, -300.f), f = ex2(d);
   a.e = f * fmaf(d, a.s, a.e);
   a.s *= f;
 }
@@ -175,11 +177,11 @@ __device__ __forceinline__ float take(Seen& t, const uint4 (&w)[kPieces], int j0
     }
     top = fmaxf(top, m);
   }
-  if (top * kL > t.a.m) {
-    lower(t.a, top * kL);
-    t.a.m = top * kL;
+  if (top > t.a.m) {
+    lower(t.a, top);
+    t.a.m = top;
   }
-  const float off = t.a.m == -INFINITY ? 0.f : -t.a.m;
+  const float off = -finite_or_0(t.a.m);
   const uint64_t by = f2pack(kL, kL), off2 = f2pack(off, off);
   uint64_t s[2] = {0, 0}, e[2] = {0, 0};
   const T* p = nullptr;
@@ -189,7 +191,7 @@ __device__ __forceinline__ float take(Seen& t, const uint4 (&w)[kPieces], int j0
     floats_of(w[b], p, x);
 #pragma unroll
     for (int i = 0; i < kPer<T>; i += 2) {
-      const uint64_t y2 = ffma2(f2pack(x[i], x[i + 1]), by, off2);
+      const uint64_t y2 = fmul2(fadd2(f2pack(x[i], x[i + 1]), off2), by);
       float y0, y1;
       f2unpack(y2, y0, y1);
       const uint64_t w2 = f2pack(ex2(y0), ex2(y1));
@@ -199,7 +201,7 @@ __device__ __forceinline__ float take(Seen& t, const uint4 (&w)[kPieces], int j0
   }
   t.a.s += f2sum(fadd2(s[0], s[1]));
   float weighted = f2sum(fadd2(e[0], e[1]));
-  if (weighted != weighted) {  // an entry of -inf, 0 times it: again, with what has no weight held (or NaN, which stays)
+  if (weighted != weighted) {  // a y of -inf, 0 times it: again, with what has no weight held (or NaN, which stays)
     weighted = 0.f;
 #pragma unroll
     for (int b = 0; b < kPieces; ++b) {
@@ -207,7 +209,7 @@ __device__ __forceinline__ float take(Seen& t, const uint4 (&w)[kPieces], int j0
       floats_of(w[b], p, x);
 #pragma unroll
       for (int i = 0; i < kPer<T>; ++i) {
-        const float y = fmaf(x[i], kL, off);
+        const float y = (x[i] + off) * kL;
         weighted = fmaf(ex2(y), fmaxf(y, -200.f), weighted);
       }
     }
@@ -225,12 +227,11 @@ __device__ __forceinline__ float take_edge(Seen& t, const Row<T>& row, int j) {
       t.best = x[i];
       t.piece = j;
     }
-    const float top = x[i] * kL;
-    if (top > t.a.m) {
-      lower(t.a, top);
-      t.a.m = top;
+    if (x[i] > t.a.m) {
+      lower(t.a, x[i]);
+      t.a.m = x[i];
     }
-    const float y = fmaf(x[i], kL, t.a.m == -INFINITY ? 0.f : -t.a.m), w = ex2(y);
+    const float y = (x[i] - finite_or_0(t.a.m)) * kL, w = ex2(y);
     t.a.s += w;
     t.a.e = fmaf(w, fmaxf(y, -200.f), t.a.e);
     most = fmaxf(most, x[i]);
@@ -451,8 +452,8 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSM<kWarps>) logprobs_kernel(c
     cluster_sync();  // no CTA leaves while its shared memory is read
     if (at != 0) return;
   }
-  const float off = sum.m == -INFINITY ? 0.f : -sum.m, log_s = log2f(sum.s);
-  auto logprob = [&](float x) { return (fmaf(x, kL, off) - log_s) * kLn2; };
+  const float log_s = log2f(sum.s);
+  auto logprob = [&](float x) { return fmaf(-log_s, kLn2, x - finite_or_0(sum.m)); };
   if (tid == 0) {
     if (a.logprobs && a.tokens) a.logprobs[r] = token < a.V ? logprob(to_f(row.p[token])) : -INFINITY;
     if (a.entropy) a.entropy[r] = (log_s - sum.e / sum.s) * kLn2;
