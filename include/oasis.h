@@ -883,8 +883,10 @@ OASIS_API int oasis_q8_keep(oasis_q8* q8, int num_requests, int num_nodes, const
  * A row with tokens[r] < 0 is not wanted: it is not read and its outputs are
  * left as they are.  Entries of -infinity have probability 0.  Rows with NaN
  * or +infinity, or nothing above -infinity, give NaN (of the first kinds ids
- * are unspecified).  Sums are fp32: a value is off by at most 2^-19 + 2^-21 of
- * itself and 2^-22 (x_max - x) for a token's x. */
+ * are unspecified).  Entries may be as large as their type's.  Sums are fp32 and
+ * carry their rounding along: whatever V, a log probability is off by at most
+ * 2^-17 + 2^-21 of itself + 2^-22 (x_max - x) for the token's x, an entropy by
+ * 2^-17 + 2^-17 of itself (in common rows 2^-20 and less). */
 typedef struct {
   int32_t num_rows;       /* 0..2^24 */
   int32_t vocab;          /* V, 1..2^20 */

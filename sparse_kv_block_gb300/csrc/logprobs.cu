@@ -4,10 +4,16 @@
 // With x a row, m its maximum and S = sum e^(x - m):
 //   log p_i = (x_i - m) - log S,   H = log S - sum e^(x - m) (x - m) / S,
 // both from one pass that keeps m, S and the weighted sum (in powers of two),
-// and every thread's largest entry.  H is a sum of two terms >= 0, so nothing
-// cancels.  m is kept as it is, and x - m formed before anything else: a product
+// and every thread's largest entry.  H is a sum of two terms >= 0 (m lags behind
+// the maximum by a factor of 2^4 at most, so but for 4), so nothing much cancels.
+// m is kept as it is, and x - m formed before anything else: a product
 // with log2 e would be off by more than whole powers of two from |x| of 10^8 on
 // and overflow near the type's largest, where masks are.
+//
+// Roundings of S, in 2^-24 of it: 4 of a weight, 9 in a group of entries, 2 of the
+// running sum, 24 where m is moved while what was summed still counts, three
+// lowerings of 5 and 11 additions where threads, warps and CTAs are joined: 65, and
+// 2.2 times the mean of |y| (under 13) for the y's.
 //
 // The k largest.  Entries are ordered by (value, then lower index), as 64-bit
 // keys, so no two are equal.  The k-th largest of the threads' own largest
@@ -43,7 +49,8 @@ constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
 constexpr float kL = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// A sum of 2^y and one of 2^y y, y = (x - m) L, m the largest x.
+// A sum of 2^y and one of 2^y y, y = (x - m) L, m the largest x but for a few
+// powers of two.
 struct Sums {
   float m, s, e;
 };
@@ -55,15 +62,20 @@ __device__ __forceinline__ void lower(Sums& a, float m2) {
   a.e = f * fmaf(d, a.s, a.e);
   a.s *= f;
 }
-__device__ __forceinline__ Sums join(Sums a, Sums b) {
-  const float m = fmaxf(a.m, b.m);
+// The sums of the warp's lanes, or of each kLanes of them, as one.  (The maximum
+// first: so each is lowered, and rounded, once.)
+template <int kLanes = 32>
+__device__ __forceinline__ Sums joined(Sums a) {
+  float m = a.m;
+#pragma unroll
+  for (int off = kLanes / 2; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   lower(a, m);
-  lower(b, m);
-  return {m, a.s + b.s, a.e + b.e};
-}
-__device__ __forceinline__ Sums shuffled(const Sums& a, int off) {
-  return {__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
-          __shfl_xor_sync(0xffffffffu, a.e, off)};
+#pragma unroll
+  for (int off = kLanes / 2; off; off >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, off);
+    a.e += __shfl_xor_sync(0xffffffffu, a.e, off);
+  }
+  return {m, a.s, a.e};
 }
 
 template <typename T>
@@ -137,12 +149,38 @@ __device__ __forceinline__ uint64_t key_of(float x, int at) {
   return static_cast<uint64_t>(float_key(x)) << 32 | static_cast<uint32_t>(~at);
 }
 
-// What a thread has seen: its sums, and the piece with its largest entry.
+// What a thread has seen: its sums, and the piece with its largest entry.  A
+// thread of a long row adds up to 512 times, equal entries with roundings of one
+// sign: so each sum's rounding is carried along into the next addition (over:
+// what the sums are too large by).
 struct Seen {
   Sums a{-INFINITY, 0.f, 0.f};
+  float over_s = 0.f, over_e = 0.f;
   float best = -INFINITY;
   int piece = -1;
 };
+__device__ __forceinline__ void settle(Seen& t) {
+  t.a.s -= t.over_s;
+  t.a.e -= t.over_e;
+  t.over_s = t.over_e = 0.f;
+}
+__device__ __forceinline__ void add(Seen& t, float s, float e) {
+  const float ds = s - t.over_s, de = e - t.over_e;
+  const float to_s = t.a.s + ds, to_e = t.a.e + de;
+  t.over_s = (to_s - t.a.s) - ds;
+  t.over_e = (to_e - t.a.e) - de;
+  t.a.s = to_s;
+  t.a.e = to_e;
+}
+// An entry x is to be added.  (The maximum is left where it is until weights would
+// pass 2^4: each time it is moved rounds the sums.)
+__device__ __forceinline__ void reach(Seen& t, float x) {
+  if ((x - t.a.m) * kL > 4.f) {
+    settle(t);
+    lower(t.a, x);
+    t.a.m = x;
+  }
+}
 
 // Two entries a word, their largest, and as floats (an fp32 row: one a word).
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, const __nv_bfloat16*) {
@@ -177,10 +215,7 @@ __device__ __forceinline__ float take(Seen& t, const uint4 (&w)[kPieces], int j0
     }
     top = fmaxf(top, m);
   }
-  if (top > t.a.m) {
-    lower(t.a, top);
-    t.a.m = top;
-  }
+  reach(t, top);
   const float off = -finite_or_0(t.a.m);
   const uint64_t by = f2pack(kL, kL), off2 = f2pack(off, off);
   uint64_t s[2] = {0, 0}, e[2] = {0, 0};
@@ -199,7 +234,6 @@ __device__ __forceinline__ float take(Seen& t, const uint4 (&w)[kPieces], int j0
       e[i >> 1 & 1] = ffma2(w2, y2, e[i >> 1 & 1]);
     }
   }
-  t.a.s += f2sum(fadd2(s[0], s[1]));
   float weighted = f2sum(fadd2(e[0], e[1]));
   if (weighted != weighted) {  // a y of -inf, 0 times it: again, with what has no weight held (or NaN, which stays)
     weighted = 0.f;
@@ -214,7 +248,7 @@ __device__ __forceinline__ float take(Seen& t, const uint4 (&w)[kPieces], int j0
       }
     }
   }
-  t.a.e += weighted;
+  add(t, f2sum(fadd2(s[0], s[1])), weighted);
   return top;
 }
 // The same of one piece that may be partly outside the row.
@@ -227,13 +261,9 @@ __device__ __forceinline__ float take_edge(Seen& t, const Row<T>& row, int j) {
       t.best = x[i];
       t.piece = j;
     }
-    if (x[i] > t.a.m) {
-      lower(t.a, x[i]);
-      t.a.m = x[i];
-    }
+    reach(t, x[i]);
     const float y = (x[i] - finite_or_0(t.a.m)) * kL, w = ex2(y);
-    t.a.s += w;
-    t.a.e = fmaf(w, fmaxf(y, -200.f), t.a.e);
+    add(t, w, w * fmaxf(y, -200.f));
     most = fmaxf(most, x[i]);
   }
   return most;
@@ -419,22 +449,21 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSM<kWarps>) logprobs_kernel(c
     for (int b = 0; b < kBatch; ++b) w[b] = next[b];
   }
 
-  Sums sum = t.a;
-#pragma unroll
-  for (int off = 16; off; off >>= 1) sum = join(sum, shuffled(sum, off));
+  settle(t);
+  Sums sum = joined(t.a);
   if (lane == 0) sh.warp_sum[warp] = sum;
   __syncthreads();
-  sum = sh.warp_sum[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) sum = join(sum, sh.warp_sum[w]);
+  sum = joined<kWarps>(sh.warp_sum[lane % kWarps]);
   if (a.k > 0) largest(sh, row, t, a.k, first, total, slot);
 
   if (cluster > 1) {
     if (tid == 0) sh.sum = sum;
     cluster_sync();
     if (at == 0) {
-      for (int c = 1; c < cluster; ++c)
-        sum = join(sum, Sums{load_remote(&sh.sum.m, c), load_remote(&sh.sum.s, c), load_remote(&sh.sum.e, c)});
+      Sums of{-INFINITY, 0.f, 0.f};  // a CTA of the cluster
+      if (const int c = lane % kMaxCluster; c < cluster)
+        of = {load_remote(&sh.sum.m, c), load_remote(&sh.sum.s, c), load_remote(&sh.sum.e, c)};
+      sum = joined<kMaxCluster>(of);
       if (a.k > 0) {
         for (int i = tid; i < cluster * kTop; i += kThreads) {
           const uint64_t* from = &sh.result[i % kTop];
