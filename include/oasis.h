@@ -843,8 +843,8 @@ OASIS_API int oasis_q8_append(oasis_q8* q8, const oasis_rope* rope, const void* 
  * nothing, and those of a request with no tokens, give zeros; so do those of a
  * request with fewer tokens than nodes, which raises BAD_BLOCK_ID.
  * num_requests <= 65535, R * N * Hq < 2^31.
- * Precision: scores, maxima and sums are fp32; a query's entries count to 2^-19
- * of its row's largest (exactly those within 2^-10 of it in bf16, 2^-7 in fp16).
+ * Precision: scores, maxima and sums are fp32; a query's entries count to 2^-17.8
+ * of its row's largest (exactly those within 2^-9 of it in bf16, 2^-6 in fp16).
  * Weights are fp16 (2^-11 each, or 2^-32 of the row's largest where that is
  * more).  Values of a context are kept to 2^-39 of 448 times the largest power
  * of two among theirs.  What nodes hold that a row does not see costs it

@@ -10,8 +10,9 @@
 // * Keys go in as e4m3 with their exponent bytes (kind::mxf8f6f4, scales in
 //   tensor memory), so scores come out whole.  A query row is a sum of e4m3 rows
 //   times one power of two: two of them hold bf16's eight bits, three fp16's
-//   eleven (exact for entries down to 2^-10 and 2^-7 of the row's largest; below,
-//   off by at most 2^-19 of it).  A tile of 128 tokens is eight units, whose even
+//   eleven (exact for entries down to 2^-9 and 2^-6 of the row's largest; below,
+//   off by half of e4m3's least step, 2^-10, where the largest is over 224: 2^-17.8
+//   of it).  A tile of 128 tokens is eight units, whose even
 //   and odd tokens are two operands of 64 tokens: the odd ones have their
 //   halves exchanged, which costs nothing but another order of the steps.
 // * Values have a unit's 16 tokens consecutive, which is an operand's layout
