@@ -869,7 +869,9 @@ OASIS_API int oasis_q8_tree_workspace(const oasis_q8* q8, int num_requests, int 
  * any order and name a node twice).  nodes: dev [R][M] int32, keep: dev [R]
  * int32, held to 0..min(M, n_r); num_nodes, tree_size and seq_len as above
  * (before they are lowered).  A node outside 0..n_r - 1 raises BAD_UNIT and its
- * place stays as it is; a bad page or a length under n_r BAD_BLOCK_ID.
+ * place stays as it is; a bad page BAD_BLOCK_ID, as a length under n_r or past
+ * the table does where something is to be kept, and then nothing moves.  A length
+ * of 0 or less is an empty request, as everywhere, and raises nothing.
  * max_keep = M, 1..64.  A page must not be in two requests' trees. */
 OASIS_API int oasis_q8_keep(oasis_q8* q8, int num_requests, int num_nodes, const int32_t* tree_size,
                             const int32_t* page_table, const int32_t* seq_len, const int32_t* nodes,
