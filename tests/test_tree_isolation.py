@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests import _q8 as Q
+from sparse_kv_block_gb300 import oasis as ob
 from tests import _tree as T
 from tests.test_q8 import BF, HF, dev, gen  # noqa: F401
 from tests.test_tree_attn import case, go
@@ -85,3 +85,16 @@ def test_every_node_of_another_size(dev, before):  # noqa: F811
             o, bound = row_of(s, pages, r, i, N)
             off = np.abs(got[r, i] - o)
             assert (off <= bound).all(), (r, i, (off / bound).max())
+
+
+def test_wide_context_around_a_bad_page(dev):  # noqa: F811
+    """A block that is left out makes its tile one that is looked at token by token; the context's
+    values there are up to 2^60 apart."""
+    s = case(2, 6, 8, 2, [400, 150], gen(17), fp32=True, amp=0.5, spread=8.0)
+    s["table"][0, 3], s["table"][1, 1] = -1, 10000
+    go(s)
+    with pytest.raises(ob.OasisError, match="0x1"):
+        s["c"].oasis_q8_sync()
+    o, bound, _ = T.attention(s["q"], s["words"], None, s["pages"], s["table"], s["lens"], None, s["out"].dtype)
+    off = np.abs(s["out"].double().cpu().numpy() - o)
+    assert (off <= bound).all(), (off / bound).max()
