@@ -821,11 +821,12 @@ OASIS_API const char* oasis_rope_error(const oasis_rope* rope);
  * in another way.  q and q_out may be NULL (keys alone).  positions: dev
  * [num_axes][T] int64, any values.  Tokens with a negative slot are not
  * written; their queries are turned all the same.
- * Precision: an angle is off by at most 2^-27 of a
- * turn for positions up to 2^32; turning is fp32, rounded once, to q_out's type and to codes: keys are
- * not rounded to `type` between.  A row whose largest value comes within
- * fp32's rounding of a border of two exponents may get either.  The values are
- * oasis_q8_write's. */
+ * Precision: an angle is off by at most 2^-27 of a turn for positions up to
+ * 2^32; turning is fp32, rounded once, to q_out's type and to codes: keys are
+ * not rounded to `type` between.  What turning takes past fp32's range is an
+ * infinity, and an infinite entry makes its pair infinite or NaN.  A row whose
+ * largest value comes within fp32's rounding of a border of two exponents may
+ * get either.  The values are oasis_q8_write's. */
 OASIS_API int oasis_q8_append(oasis_q8* q8, const oasis_rope* rope, const void* q, void* q_out,
                               const void* k, const void* v, int type, int64_t q_stride,
                               int64_t q_out_stride, int64_t k_stride, int64_t v_stride,

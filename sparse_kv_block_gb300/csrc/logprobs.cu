@@ -22,12 +22,16 @@
 // threshold (some k of them) are read again, and their entries that reach it are
 // ranked by counting.  Nothing depends on the order in which threads get there.
 //
-// Bound by memory, and by its integer and fp32 pipes in 16-bit types (some four
-// operations an entry); a thread's next four pieces are on their way while four
-// are looked at.  GB300, 512 rows of 151936, bf16: k = 0 41 us, 1 42, 20 44 (3.5
-// TB/s); fp32, k = 20, 75 (4.1 TB/s).  Before: without the next pieces on their
-// way and packed arithmetic 47; the entries of the k threads read again, 20 us
-// more at k = 20 (16 bytes of each sector of memory that has left the L2).
+// Bound by memory in fp32 without alternatives, else by latency: no pipe is busy
+// over 41 % of the time, 49 % of the issue slots are used, 44 % of the memory's
+// rate (bf16, k = 20), and all CTAs of the one wave read, then rank, at the same
+// time.  A thread's next four pieces are on their way while four are looked at.
+// GB300, 512 rows of 151936, calls in a row: bf16 k = 0 36 us, 1 40, 20 47 (3.3
+// TB/s); fp32 k = 0 51 (6.1 TB/s), 20 61; bf16, k = 20, all but a thousandth -inf 57
+// (the weighted sum is formed twice).  x - m in place of one multiply-add costs 2
+// of the 47.  On the way (of then 44): without the next pieces on their way and
+// packed arithmetic 47; the entries of the k threads read again, 20 us more at k =
+// 20 (16 bytes of each sector of memory that has left the L2).
 #include <cuda_fp16.h>
 
 #include "q8.cuh"
@@ -38,8 +42,10 @@ namespace {
 
 // Warps a CTA: eight where the clusters of eight CTAs of all rows run at once (a
 // row's latency counts), else four, whose CTAs fill the SMs more evenly.  GB300,
-// us with four and eight: 4 rows of 32000, k = 5, 11.1, 9.9; 1 of 151936, k = 1,
-// 17.0, 15.0; 64 of 128256, k = 20, 27.3, 33.4 (two rounds).
+// calls in a row, us with four and eight: 4 rows of 32000, fp32, k = 5, 10.7, 9.2; 1
+// of 151936, bf16, k = 1, 10.5, 8.6; 256 of 128256, k = 20, 27.7, 30.5; 512 of 151936
+// 46.5, 50.3.  Just past the rule's border, of 57 rows, eight would still be better:
+// 64 of 128256, k = 20, 26.6, 17.7 (clusters of eight and of four CTAs).
 constexpr int kFewRows = 8, kManyRows = 4;
 template <int kWarps>
 constexpr int kPerSM = 28 / kWarps;  // CTAs

@@ -37,12 +37,17 @@
 // end.  A job is 128 rows x 64 tokens; its scores are in one of three buffers of
 // tensor memory, where its weights take their place.
 //
-// GB300, us: 16 requests x 64 nodes x 32 / 8 heads over 16384 tokens 243 (tensor
-// cores 146 at the measured bf16 rate), 24 ragged ones up to 9001 tokens, fp16,
-// 73, one of 16 nodes over 4096 21.  What holds it back is a job's way through
-// the buffers (scores 400 cycles, the softmax of its 64 columns 700 to 1000,
-// outputs 270, 100 to 300 from each hand to the next): 960 cycles a job where
-// the products alone take 640.  Measured on the way, the first case: 128 columns a
+// GB300, us: 16 requests x 64 nodes x 32 / 8 heads over 16384 tokens 241 (tensor
+// cores 146 at the measured bf16 rate), in fp16 320 (its pages are read twice), 24
+// ragged ones up to 9001 tokens, fp16, 73, one of 16 nodes over 4096 22.  With many
+// rows what holds it back is a job's way through the buffers (scores 400 cycles,
+// 384 of them for the operands that its steps of 64 columns read from shared
+// memory; the softmax of its 64 columns 700 to 1000, outputs 270, 100 to 300 from
+// each hand to the next): 960 cycles a job where the products alone take 640.  With
+// few rows it is the loads (16 x 4 nodes 160, as the large case with nothing but its
+// loads: 3.4 TB/s), in ragged batches also what a segment begins and ends with,
+// some 9000 cycles that nothing covers and the share-out does not count.  Measured
+// on the way, the first case (of then 243): 128 columns a
 // job and two buffers 288; two buffers for scores and three for weights, released
 // as soon as they are read, 278; sixteen softmax warps 317; more registers for
 // the softmax warps (setmaxnreg) spilled.  The elected lane must not change in
